@@ -87,6 +87,8 @@ typedef enum {
 
 typedef enum { HARP_THETA_F32 = 0, HARP_THETA_I8 = 1 } harp_theta_kind;
 typedef enum { HARP_F32 = 0, HARP_BF16 = 1 } harp_dtype;
+/* 8-bit codes: int8 (Q = 127) or e4m3 (Q = 448, the largest finite value); see harp_quantize. */
+typedef enum { HARP_CODE_I8 = 0, HARP_CODE_E4M3 = 1 } harp_code;
 /* FORWARD: y = T x.  INVERSE: y = T^T x (exact inverse; T is orthogonal). */
 typedef enum { HARP_FORWARD = 0, HARP_INVERSE = 1 } harp_dir;
 
@@ -203,6 +205,94 @@ HARP_API harp_status harp_apply_quant(harp_plan_t plan, const void* x, int64_t r
                                       int64_t ld_s, int32_t qblock, harp_dir dir, void* stream);
 
 /*
+ * harp_apply_quant_ex — harp_apply_quant with the code format chosen by the caller.
+ * HARP_CODE_I8 is harp_apply_quant itself.  HARP_CODE_E4M3 writes e4m3 codes with the rules of
+ * harp_quantize (Q = 448; a row that holds a NaN or an infinity keeps it in its scales): the row
+ * operand of harp_matmul_quant when qblock = 128.  Kernels, alignment and errors as
+ * harp_apply_quant; harp_apply_quant takes no NaN into its scales.
+ */
+HARP_API harp_status harp_apply_quant_ex(harp_plan_t plan, const void* x, int64_t rows, int64_t ld_x,
+                                         harp_dtype in_dtype, harp_code code, void* q, int64_t ld_q,
+                                         float* scales, int64_t ld_s, int32_t qblock, harp_dir dir,
+                                         void* stream);
+
+/*
+ * harp_quantize — 8-bit codes of a matrix with one fp32 scale per block (§2.4: the
+ * blockwise quantizer behind the rotation).  For every block with maximum magnitude a:
+ *   s = a / Q,  code = rne(v * (Q / a))     (fp32, each operation rounded to nearest;
+ *                                            Q = 127 for int8, 448 for e4m3)
+ * so v ~ code * s, off by at most s / 2 (int8), or by 2^-4 |v| or s 2^-10, whichever is more
+ * (e4m3).  A block with a < 2^-100 counts as zero (s = 0, codes 0).  A block that holds a NaN or
+ * an infinity keeps it in its scale: all of the block decodes to NaN.
+ *   x        device rows x cols values, element type dtype, leading dimension ld_x >= cols.
+ *   brows x bcols   the block: 1 x 32, 64, 128 or 256 (rows kept as checkpoints for
+ *            harp_grad_theta_quant; row operand of harp_matmul_quant with 128), or 128 x 128
+ *            (its weight operand); blocks at the right and lower edges may be short.
+ *   q        device codes, one byte each, leading dimension ld_q >= cols.
+ *   scales   device float, ceil(rows / brows) x ceil(cols / bcols), leading dimension
+ *            ld_s >= ceil(cols / bcols).
+ * Any alignment (rows 16-byte aligned, codes 8-byte aligned go faster).  x, q and scales must
+ * not overlap.  rows = 0 or cols = 0 is a no-op.  Asynchronous on `stream`; no workspace.
+ */
+HARP_API harp_status harp_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld_x, harp_dtype dtype,
+                                   harp_code code, int32_t brows, int32_t bcols, void* q, int64_t ld_q,
+                                   float* scales, int64_t ld_s, void* stream);
+
+/*
+ * harp_dequantize — y = rn(code * scale) of the codes that harp_quantize (or harp_apply_quant_ex,
+ * harp_rms_norm_quant) left: the checkpoint's rows back in `dtype`.  Arguments as harp_quantize,
+ * with y in the place of x.
+ */
+HARP_API harp_status harp_dequantize(const void* q, int64_t ld_q, const float* scales, int64_t ld_s,
+                                     harp_code code, int32_t brows, int32_t bcols, int64_t rows, int64_t cols,
+                                     void* y, int64_t ld_y, harp_dtype dtype, void* stream);
+
+/*
+ * harp_rms_norm_quant — a layer's entry in front of the quantizer: residual addition,
+ * root-mean-square norm and 8-bit codes in one pass over the rows.  Per row r:
+ *   h = rn(rn32(x + residual))                (rounded to dtype; h = x without a residual)
+ *   t = rn32(1 / sqrt(sum_j h_j^2 / d + eps)) (sum, quotient and root in double, so t does not
+ *                                              depend on the order of the additions)
+ *   u = rn32(rn32(h t) weight)                (u = rn32(h t) without a weight)
+ * and u's codes and scales per block of qblock coordinates, as harp_quantize of the fp32 u.
+ *   x, residual   device rows of d, element type dtype; residual may be NULL.
+ *   weight   d values of type dtype, or NULL (a weight that was folded into the next matrix).
+ *   eps      1e-70 <= eps <= 1e30.
+ *   h        NULL, or rows of d that receive h; may be x or residual itself (then with the same
+ *            leading dimension).
+ *   y        NULL, or rows of d that receive u rounded to dtype (the rows for harp_apply_quant_ex
+ *            where the layer's input is rotated).
+ *   q, scales   codes and scales as harp_quantize with 1 x qblock blocks, or both NULL.
+ * 1 <= d <= HARP_MAX_DIM.  At least one of h, y, q is given.  No other overlap is allowed.
+ * Any alignment (16-byte aligned rows, 8-byte aligned codes go faster).  rows = 0 is a no-op.
+ * Asynchronous on `stream`; no workspace.
+ */
+HARP_API harp_status harp_rms_norm_quant(const void* x, int64_t ld_x, const void* residual, int64_t ld_r,
+                                         const void* weight, int64_t rows, int64_t d, harp_dtype dtype,
+                                         double eps, void* h, int64_t ld_h, void* y, int64_t ld_y,
+                                         harp_code code, int32_t qblock, void* q, int64_t ld_q, float* scales,
+                                         int64_t ld_s, void* stream);
+
+/*
+ * harp_matmul_quant — the product of quantized rows and a quantized weight, y ~ x w^T:
+ *   y[r][j] = sum_b sx[r][b] sw[j / 128][b] sum_{i in block b} x[r][i] w[j][i]
+ * over blocks b of 128 along k (the last one may be short); e4m3 codes, products and sums in
+ * fp32, the result rounded once.
+ *   x, sx    rows x k codes (1 byte each, leading dimension ld_x >= k) and rows x ceil(k / 128)
+ *            scales (ld_sx): harp_apply_quant_ex, harp_rms_norm_quant or harp_quantize with
+ *            qblock 128.
+ *   w, sw    n x k codes (ld_w >= k) and ceil(n / 128) x ceil(k / 128) scales (ld_sw):
+ *            harp_quantize with 128 x 128 blocks of W (or of the rotated T_U^T W T_V).
+ *   y        rows x n results of type out_dtype, leading dimension ld_y >= n; overlaps nothing.
+ * Each sum's order depends on the sizes only, so equal calls give equal bits.  Any alignment
+ * (16-byte aligned operands with leading dimensions that are multiples of 16 take the tensor
+ * cores).  rows = 0 or n = 0 is a no-op; rows, n, k < 2^31.  Asynchronous on `stream`; no workspace.
+ */
+HARP_API harp_status harp_matmul_quant(const void* x, int64_t ld_x, const float* sx, int64_t ld_sx, const void* w,
+                                       int64_t ld_w, const float* sw, int64_t ld_sw, int64_t rows, int64_t n,
+                                       int64_t k, void* y, int64_t ld_y, harp_dtype out_dtype, void* stream);
+
+/*
  * harp_apply_columns — every column of an fp32 matrix takes T (FORWARD) or T^T
  * (INVERSE): for j < ncols, y[:, j] = T x[:, j] with x of d = plan dimension rows.  The
  * column side of a two-sided rotation, applied in place without a transpose (HARP
@@ -307,6 +397,19 @@ HARP_API size_t harp_grad_workspace_bytes(harp_plan_t plan);
 HARP_API harp_status harp_grad_theta(harp_plan_t plan, const void* x, const void* g, int64_t rows,
                                      int64_t ld_x, int64_t ld_g, harp_dtype dtype, float* dtheta,
                                      void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * harp_grad_theta_quant — harp_grad_theta from 8-bit checkpoints: the rows x are kept between
+ * the forward and the backward as codes and scales (harp_quantize with blocks of 1 x qblock, half
+ * the bytes of bf16 rows) and are decoded, x^ = rn32(code * scale), as the kernel reads them.
+ *   q, code, scales, qblock   the checkpoint of rows x d; qblock 32, 64, 128 or 256.
+ *   g        upstream gradients, rows of d elements of type dtype.
+ * Everything else (dtheta, workspace, arithmetic, errors) as harp_grad_theta on the rows x^.
+ */
+HARP_API harp_status harp_grad_theta_quant(harp_plan_t plan, const void* q, int64_t ld_q, harp_code code,
+                                           const float* scales, int64_t ld_s, int32_t qblock, const void* g,
+                                           int64_t ld_g, harp_dtype dtype, int64_t rows, float* dtheta,
+                                           void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * harp_off_block_energy — the block-diagonality term of the fit (§2.3 Optimization

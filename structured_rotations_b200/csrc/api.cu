@@ -1,6 +1,7 @@
 // C entry points that run device work: argument checks and dispatch between the
 // specialized and the general row kernels, and the two-sided weight rotation
 // (HARP abstract: a two-sided orthogonal processor; W_out = T_U^T W T_V).
+#include <atomic>
 #include <cstdlib>
 #include <cstring>
 #include <map>
@@ -49,6 +50,22 @@ int kernel_choice() {
 constexpr int64_t kClusterRows = 65;
 
 }  // namespace
+
+int harp_sm_count() {
+    static std::atomic<int> cached[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) dev = 0;
+    int n = cached[dev].load(std::memory_order_relaxed);
+    if (!n) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+            cudaGetLastError();
+            return 1;
+        }
+        cached[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
 
 int harp_set_smem_limit(const void* kernel, int bytes) {
     static std::mutex mu;
@@ -138,9 +155,16 @@ extern "C" harp_status harp_apply_ex(harp_plan_t p, const void* x, void* y, int6
 extern "C" harp_status harp_apply_quant(harp_plan_t p, const void* x, int64_t rows, int64_t ld_x, harp_dtype in_dtype,
                                         int8_t* q, int64_t ld_q, float* scales, int64_t ld_s, int32_t qblock,
                                         harp_dir dir, void* stream) {
+    return harp_apply_quant_ex(p, x, rows, ld_x, in_dtype, HARP_CODE_I8, q, ld_q, scales, ld_s, qblock, dir, stream);
+}
+
+extern "C" harp_status harp_apply_quant_ex(harp_plan_t p, const void* x, int64_t rows, int64_t ld_x,
+                                           harp_dtype in_dtype, harp_code code, void* q, int64_t ld_q, float* scales,
+                                           int64_t ld_s, int32_t qblock, harp_dir dir, void* stream) {
     harp_clear_error();
     if (!p) return harp_fail(HARP_ERR_INVALID_ARG, "plan is NULL");
     if (in_dtype != HARP_BF16) return harp_fail(HARP_ERR_UNSUPPORTED, "the fused quantizer takes bf16 rows");
+    if (code != HARP_CODE_I8 && code != HARP_CODE_E4M3) return harp_fail(HARP_ERR_UNSUPPORTED, "unknown code format");
     if (dir != HARP_FORWARD && dir != HARP_INVERSE) return harp_fail(HARP_ERR_UNSUPPORTED, "unknown direction");
     if (rows < 0) return harp_fail(HARP_ERR_INVALID_ARG, "rows < 0");
     const int64_t d = p->desc.d;
@@ -161,11 +185,11 @@ extern "C" harp_status harp_apply_quant(harp_plan_t p, const void* x, int64_t ro
         return harp_fail(HARP_ERR_INVALID_ARG, "x, q and scales overlap");
     const int choice = kernel_choice();
     if (choice == kAuto || choice == kFast) {
-        st = launch_apply_fast_quant(p, x, rows, ld_x, q, ld_q, scales, ld_s, qblock, dir, stream);
+        st = launch_apply_fast_quant(p, x, rows, ld_x, q, ld_q, scales, ld_s, qblock, code, dir, stream);
         if (st != HARP_ERR_UNSUPPORTED || choice == kFast) return st;
         harp_clear_error();
     }
-    QuantOut qo{scales, ld_s, qblock};
+    QuantOut qo{scales, ld_s, qblock, code};
     st = launch_apply_tiled(p, x, q, rows, ld_x, ld_q, HARP_BF16, HARP_BF16, dir, stream, &qo);
     if (st == HARP_ERR_UNSUPPORTED)
         return harp_fail(HARP_ERR_UNSUPPORTED, "the fused quantizer needs radices <= 8, d % 8 == 0, 16-byte "

@@ -34,12 +34,14 @@
 // free; the derivations are next to each index function.
 #include <cstdio>
 #include <mutex>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include "codes.cuh"
 #include "harp_internal.h"
 
 namespace {
@@ -64,7 +66,7 @@ struct FastParams {
     int ntiles;
     const float4* frag;      // B fragments, [cta rank][warp][column / 4][lane] float4 (see pack kernel)
     int* status;
-    int8_t* q;               // quantizing variant: int8 codes, rows of 4096, leading dimension ldq
+    int8_t* q;               // quantizing variant: codes, rows of 4096, leading dimension ldq
     int64_t ldq;
     float* scales;           // and one scale per block of QB coordinates, leading dimension lds
     int64_t lds;
@@ -398,13 +400,19 @@ __device__ __forceinline__ void st_async_b32(uint32_t addr, uint32_t v, uint32_t
                  : "memory");
 }
 
-template <int QB>
+// e4m3 codes (C = CodeE4M3) differ in Q = 448, in the conversion, and in keeping a NaN of the row
+// in its scales (codes.cuh; the maximum of the patterns keeps it too, a NaN's being above
+// infinity's).
+template <int QB, typename C>
 __device__ __forceinline__ void quant_row(const float* E, unsigned char* S, const FastParams& p, int64_t row0, int r,
                                           int w, int lane, uint64_t* qbar, uint32_t qparity, uint32_t remote_s,
                                           uint32_t remote_qbar) {
     constexpr int SH = QB <= 64 ? 0 : (QB == 128 ? 1 : 2);   // block of beta >> SH
     constexpr int NLOC = 64 >> SH;                           // blocks of the row in this CTA's view
     constexpr bool XCH = QB >= 64;                           // blocks span both CTAs
+    constexpr bool kE4M3 = std::is_same<C, harp_codes::CodeE4M3>::value;
+    auto larger = [](float a, float b) { return kE4M3 ? harp_codes::amax_nan(a, b) : fmaxf(a, b); };
+    auto scale_of = [](float a) { return kE4M3 ? harp_codes::code_scale<C>(a) : __fdiv_rn(a, 127.f); };
     float v[64];
 #pragma unroll
     for (int beta = 0; beta < 64; ++beta) v[beta] = E[e_index<QB>(beta >> 5, w, lane, beta)];
@@ -413,7 +421,10 @@ __device__ __forceinline__ void quant_row(const float* E, unsigned char* S, cons
     for (int kb = 0; kb < NLOC; ++kb) {
         float m = 0.f;
 #pragma unroll
-        for (int t = 0; t < (1 << SH); ++t) m = fmaxf(m, fabsf(v[(kb << SH) + t]));
+        for (int t = 0; t < (1 << SH); ++t) {
+            if constexpr (kE4M3) m = harp_codes::amax_nan(m, v[(kb << SH) + t]);
+            else m = fmaxf(m, fabsf(v[(kb << SH) + t]));
+        }
         const float wm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
         if (kb < 32) own0 = lane == kb ? wm : own0;
         else own1 = lane == kb - 32 ? wm : own1;
@@ -428,8 +439,8 @@ __device__ __forceinline__ void quant_row(const float* E, unsigned char* S, cons
             mbar_wait(qbar, qparity);   // bounded again: no store may land after exit
         }
         const float* amx = reinterpret_cast<const float*>(S + kAmxOffset) + w * 64;
-        if (lane < NLOC) a0 = fmaxf(own0, amx[lane]);
-        if (NLOC > 32) a1 = fmaxf(own1, amx[lane + 32]);
+        if (lane < NLOC) a0 = larger(own0, amx[lane]);
+        if (NLOC > 32) a1 = larger(own1, amx[lane + 32]);
     }
     float inv0 = 0.f, inv1 = 0.f;   // lane L: 127 / a of blocks L and L + 32
     const int64_t grow = row0 + w;
@@ -438,14 +449,14 @@ __device__ __forceinline__ void quant_row(const float* E, unsigned char* S, cons
         const int kb = lane + 32 * h;
         if (kb < NLOC) {
             const float a = h ? a1 : a0;
-            const float iv = a > 0.f ? __fdiv_rn(127.f, a) : 0.f;
+            const float iv = kE4M3 ? harp_codes::code_factor<C>(a) : a > 0.f ? __fdiv_rn(127.f, a) : 0.f;
             if (h) inv1 = iv;
             else inv0 = iv;
             if (grow < p.rows) {
                 if constexpr (XCH) {
-                    if (r == 0) p.scales[grow * p.lds + kb] = __fdiv_rn(a, 127.f);
+                    if (r == 0) p.scales[grow * p.lds + kb] = scale_of(a);
                 } else {
-                    p.scales[grow * p.lds + 2 * kb + r] = __fdiv_rn(a, 127.f);   // block (beta = kb, CTA r)
+                    p.scales[grow * p.lds + 2 * kb + r] = scale_of(a);   // block (beta = kb, CTA r)
                 }
             }
         }
@@ -457,10 +468,22 @@ __device__ __forceinline__ void quant_row(const float* E, unsigned char* S, cons
 #pragma unroll
     for (int kb = 0; kb < NLOC; ++kb) {
         const float iv = __shfl_sync(0xffffffffu, kb < 32 ? inv0 : inv1, kb & 31);
+        if constexpr (kE4M3 && SH > 0) {
+            // two codes per conversion
 #pragma unroll
-        for (int t = 0; t < (1 << SH); ++t) {
-            const int beta = (kb << SH) + t;
-            cs[beta * 32 + lane] = (unsigned char)(cvt_rni_sat_s8(v[beta] * iv) & 0xffu);
+            for (int t = 0; t < (1 << SH); t += 2) {
+                const int beta = (kb << SH) + t;
+                const uint32_t c2 = C::two(v[beta] * iv, v[beta + 1] * iv);
+                cs[beta * 32 + lane] = (unsigned char)(c2 & 0xffu);
+                cs[beta * 32 + 32 + lane] = (unsigned char)(c2 >> 8);
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < (1 << SH); ++t) {
+                const int beta = (kb << SH) + t;
+                const uint32_t c1 = kE4M3 ? C::one(v[beta] * iv) : cvt_rni_sat_s8(v[beta] * iv);
+                cs[beta * 32 + lane] = (unsigned char)(c1 & 0xffu);
+            }
         }
     }
     __syncwarp();
@@ -475,8 +498,8 @@ __device__ __forceinline__ void quant_row(const float* E, unsigned char* S, cons
 
 // ------------------------------------------------------------- kernel ---
 
-// QB = 0: bf16 rows out.  QB = 32 .. 256: int8 codes and per-block scales out (quant_row).
-template <int QB>
+// QB = 0: bf16 rows out.  QB = 32 .. 256: codes of format C and per-block scales out (quant_row).
+template <int QB, typename C = harp_codes::CodeI8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     harp_fast_d4096_fwd_kernel(const __grid_constant__ CUtensorMap tmap_x, FastParams p) {
     extern __shared__ unsigned char smem_raw[];
@@ -694,7 +717,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         __syncthreads();
         if constexpr (QB > 0) {
-            quant_row<QB>(E, reinterpret_cast<unsigned char*>(S), p, row0, r, warp, lane, qbar, qparity, remote_s,
+            quant_row<QB, C>(E, reinterpret_cast<unsigned char*>(S), p, row0, r, warp, lane, qbar, qparity, remote_s,
                           remote_qbar);
             if constexpr (QB >= 64) qparity ^= 1;
         }
@@ -764,10 +787,22 @@ bool is_d4096_radix8(const harp_plan_s* p) {
     return true;
 }
 
-// The variants: bf16 rows out, then int8 codes for quantizer blocks of 32, 64, 128, 256.
-const void* const kKernels[] = {(const void*)harp_fast_d4096_fwd_kernel<0>, (const void*)harp_fast_d4096_fwd_kernel<32>,
-                                (const void*)harp_fast_d4096_fwd_kernel<64>, (const void*)harp_fast_d4096_fwd_kernel<128>,
-                                (const void*)harp_fast_d4096_fwd_kernel<256>};
+// The variants: bf16 rows out, then int8 codes and e4m3 codes for quantizer blocks of 32, 64, 128, 256.
+using FastKernel = void (*)(const CUtensorMap, FastParams);
+const FastKernel kKernels[] = {harp_fast_d4096_fwd_kernel<0>,
+                               harp_fast_d4096_fwd_kernel<32>,
+                               harp_fast_d4096_fwd_kernel<64>,
+                               harp_fast_d4096_fwd_kernel<128>,
+                               harp_fast_d4096_fwd_kernel<256>,
+                               harp_fast_d4096_fwd_kernel<32, harp_codes::CodeE4M3>,
+                               harp_fast_d4096_fwd_kernel<64, harp_codes::CodeE4M3>,
+                               harp_fast_d4096_fwd_kernel<128, harp_codes::CodeE4M3>,
+                               harp_fast_d4096_fwd_kernel<256, harp_codes::CodeE4M3>};
+
+FastKernel variant(int qb, harp_code code) {
+    const int at = qb == 0 ? 0 : qb == 32 ? 1 : qb == 64 ? 2 : qb == 128 ? 3 : 4;
+    return kKernels[at && code == HARP_CODE_E4M3 ? at + 4 : at];
+}
 
 // The coefficient table and the launch attributes of the specialized kernel, built once per
 // plan by materialization (on the materializing stream): afterwards launches only read
@@ -783,8 +818,8 @@ harp_status prepare(harp_plan_s* p, cudaStream_t stream) {
     });
     if (!g_encode) return harp_fail(HARP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
     cudaError_t e = cudaSuccess;
-    for (const void* k : kKernels) {
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    for (FastKernel k : kKernels) {
+        e = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
         if (e != cudaSuccess) {
             cudaGetLastError();
             return harp_fail(HARP_ERR_CUDA, cudaGetErrorString(e));
@@ -795,9 +830,9 @@ harp_status prepare(harp_plan_s* p, cudaStream_t stream) {
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     int nclusters = 0;
-    for (const void* k : kKernels) {   // the variants' limits (equal in practice: one CTA per SM)
+    for (FastKernel k : kKernels) {   // the variants' limits (equal in practice: one CTA per SM)
         int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, k, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&n, (const void*)k, &cfg);
         if (e != cudaSuccess) break;
         nclusters = k == kKernels[0] ? n : std::min(nclusters, n);
     }
@@ -832,9 +867,9 @@ harp_status prepare(harp_plan_s* p, cudaStream_t stream) {
 
 namespace {
 
-// Encodes the input map and launches variant QB (0: bf16 rows to fp.y; else the quantizer).
+// Encodes the input map and launches variant QB (0: bf16 rows to fp.y; else the quantizer to codes).
 harp_status launch_variant(harp_plan_s* p, const void* x, int64_t rows, int64_t ld_x, FastParams fp, int qb,
-                           cudaStream_t stream) {
+                           harp_code code, cudaStream_t stream) {
     const FastState* fs = static_cast<const FastState*>(p->fast);
     if (!fs || !fs->ready) return HARP_ERR_UNSUPPORTED;   // no table: the plan was not eligible or it failed
     const int64_t ntiles = (rows + kTile - 1) / kTile;
@@ -863,14 +898,7 @@ harp_status launch_variant(harp_plan_s* p, const void* x, int64_t rows, int64_t 
     fp.ntiles = (int)ntiles;
     fp.frag = reinterpret_cast<const float4*>(fs->frag);
     fp.status = p->d_status;
-    switch (qb) {
-        case 0: harp_fast_d4096_fwd_kernel<0><<<2 * pairs, kThreads, kSmemBytes, stream>>>(tmap, fp); break;
-        case 32: harp_fast_d4096_fwd_kernel<32><<<2 * pairs, kThreads, kSmemBytes, stream>>>(tmap, fp); break;
-        case 64: harp_fast_d4096_fwd_kernel<64><<<2 * pairs, kThreads, kSmemBytes, stream>>>(tmap, fp); break;
-        case 128: harp_fast_d4096_fwd_kernel<128><<<2 * pairs, kThreads, kSmemBytes, stream>>>(tmap, fp); break;
-        case 256: harp_fast_d4096_fwd_kernel<256><<<2 * pairs, kThreads, kSmemBytes, stream>>>(tmap, fp); break;
-        default: return HARP_ERR_UNSUPPORTED;
-    }
+    variant(qb, code)<<<2 * pairs, kThreads, kSmemBytes, stream>>>(tmap, fp);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return harp_fail(HARP_ERR_CUDA, cudaGetErrorString(e));
     harp_set_last_kernel("harp_fast_d4096_fwd_kernel");
@@ -890,12 +918,12 @@ harp_status launch_apply_fast(harp_plan_s* p, const void* x, void* y, int64_t ro
     FastParams fp = {};
     fp.y = reinterpret_cast<__nv_bfloat16*>(y);
     fp.ldy = ld_y;
-    return launch_variant(p, x, rows, ld_x, fp, 0, (cudaStream_t)stream);
+    return launch_variant(p, x, rows, ld_x, fp, 0, HARP_CODE_I8, (cudaStream_t)stream);
 }
 
-harp_status launch_apply_fast_quant(harp_plan_s* p, const void* x, int64_t rows, int64_t ld_x, int8_t* q,
-                                    int64_t ld_q, float* scales, int64_t ld_s, int qblock, harp_dir dir,
-                                    void* stream) {
+harp_status launch_apply_fast_quant(harp_plan_s* p, const void* x, int64_t rows, int64_t ld_x, void* q,
+                                    int64_t ld_q, float* scales, int64_t ld_s, int qblock, harp_code code,
+                                    harp_dir dir, void* stream) {
     if (!is_d4096_radix8(p) || dir != HARP_FORWARD) return HARP_ERR_UNSUPPORTED;
     if (qblock != 32 && qblock != 64 && qblock != 128 && qblock != 256) return HARP_ERR_UNSUPPORTED;
     // TMA input boxes: 16-byte aligned rows; codes leave as 16-byte stores; scales as floats
@@ -903,11 +931,11 @@ harp_status launch_apply_fast_quant(harp_plan_s* p, const void* x, int64_t rows,
         return HARP_ERR_UNSUPPORTED;
     if (rows < 32 || rows > 0x7fffffffll) return HARP_ERR_UNSUPPORTED;
     FastParams fp = {};
-    fp.q = q;
+    fp.q = (int8_t*)q;
     fp.ldq = ld_q;
     fp.scales = scales;
     fp.lds = ld_s;
-    return launch_variant(p, x, rows, ld_x, fp, qblock, (cudaStream_t)stream);
+    return launch_variant(p, x, rows, ld_x, fp, qblock, code, (cudaStream_t)stream);
 }
 
 void fast_prepare(harp_plan_s* p, void* stream) {

@@ -211,7 +211,9 @@ harp_status launch_apply_tiled(const harp_plan_s* p, const void* x, void* y, int
     cudaStream_t s = (cudaStream_t)stream;
     const bool inv = dir == HARP_INVERSE;
     cudaError_t e;
-    if (quant)
+    if (quant && quant->code == HARP_CODE_E4M3)
+        e = harp_tiled_launch_bf16_e4m3(which, V, nt, cl, inv, tp, smem, grid, s);
+    else if (quant)
         e = harp_tiled_launch_bf16_i8(which, V, nt, cl, inv, tp, smem, grid, s);
     else if (in_dtype == HARP_BF16 && out_dtype == HARP_BF16)
         e = harp_tiled_launch_bf16(which, V, nt, cl, inv, tp, smem, grid, s);

@@ -31,8 +31,10 @@
 #include <type_traits>
 
 #include <cuda_bf16.h>
+#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include "codes.cuh"
 #include "harp_internal.h"
 
 namespace harp_tiled {
@@ -68,7 +70,7 @@ struct TiledParams {
     FastDiv nb_div[HARP_MAX_STAGES];   // division by (coordinates per CTA) / b_t
     FastDiv s_div[HARP_MAX_STAGES];    // division by s_t
     const float* last_blocks;          // slab mode: plain 2 x 2 blocks of the last stage
-    float* scales;                     // quantized output (int8 codes in y): per-block scales
+    float* scales;                     // quantized output (8-bit codes in y): per-block scales
     int64_t ld_s;                      // scales per row of the scales array (row stride)
     int qlanes;                        // quantizer block / 8: lanes that hold one block
     int fuse_first, fuse_last;         // stage applied while filling / draining the tile (kFuse*)
@@ -660,7 +662,34 @@ __device__ __forceinline__ void drain_tile_fused(const float4* tile, int d, int 
 // s = a / 127 and int8 codes q = clamp(rne(y * (127 / a)), -127, 127) (the quotient and the
 // reciprocal rounded to nearest in fp32; s = 0 and q = 0 for an all-zero block).  The
 // qlanes consecutive lanes that hold a block, 8 coordinates each, reduce its maximum with
-// shuffles; the NR rows a thread holds reduce in the same shuffle rounds.
+// shuffles; the NR rows a thread holds reduce in the same shuffle rounds.  e4m3 codes
+// (TOut = __nv_fp8_e4m3) follow codes.cuh instead: Q = 448, NaN and infinity kept in the scale.
+template <typename TOut>
+constexpr bool is_code = std::is_same<TOut, int8_t>::value || std::is_same<TOut, __nv_fp8_e4m3>::value;
+
+template <int NR>
+__device__ __forceinline__ void quant_rows(const float (&v)[NR][8], int nrows, __nv_fp8_e4m3* dst, int64_t ld,
+                                           float* sdst, int64_t ld_s, int qlanes, unsigned mask, bool lead) {
+    using namespace harp_codes;
+    float a[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        a[r] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) a[r] = amax_nan(a[r], v[r][k]);
+    }
+    for (int o = 1; o < qlanes; o <<= 1) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) a[r] = amax_nan(a[r], __shfl_xor_sync(mask, a[r], o));
+    }
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        if (r >= nrows) break;
+        store_codes8<CodeE4M3>((uint8_t*)(dst + r * ld), 8, true, v[r], code_factor<CodeE4M3>(a[r]));
+        if (lead) sdst[r * ld_s] = code_scale<CodeE4M3>(a[r]);
+    }
+}
+
 template <int NR>
 __device__ __forceinline__ void quant_rows(const float (&v)[NR][8], int nrows, int8_t* dst, int64_t ld, float* sdst,
                                            int64_t ld_s, int qlanes, unsigned mask, bool lead) {
@@ -690,8 +719,8 @@ __device__ __forceinline__ void quant_rows(const float (&v)[NR][8], int nrows, i
     }
 }
 
-template <int V, int NT>
-__device__ __forceinline__ void drain_tile_quant(const typename VecOf<V>::T* tile, int d, int nr, int8_t* dst,
+template <int V, int NT, typename TOut>
+__device__ __forceinline__ void drain_tile_quant(const typename VecOf<V>::T* tile, int d, int nr, TOut* dst,
                                                  int64_t ld, int mask, float* sdst, int64_t ld_s, int qlanes) {
     const int d8 = d / 8;
     const int lane = threadIdx.x & 31;
@@ -853,8 +882,8 @@ __global__ void __launch_bounds__(NT, 1) harp_tiled_kernel(const __grid_constant
         if (early && t_next < p.ntiles && step0 < step1)   // the next tile's, in flight during drain and fill
             prefetch_first<MASK, V, NT>(p, t_first, (int)((min((int64_t)R, p.rows - t_next * R) + V - 1) / V), dl,
                                         rank, w);
-        if constexpr (std::is_same<TOut, int8_t>::value)
-            drain_tile_quant<V, NT>(tile, dl, nr, (int8_t*)p.y + row0 * p.ld_y, p.ld_y, p.mask,
+        if constexpr (is_code<TOut>)
+            drain_tile_quant<V, NT>(tile, dl, nr, (TOut*)p.y + row0 * p.ld_y, p.ld_y, p.mask,
                                     p.scales + row0 * p.ld_s, p.ld_s, p.qlanes);
         else if constexpr (FUSED) {
             if (p.fuse_last)
@@ -892,7 +921,7 @@ cudaError_t launch_mask(int which, const TiledParams& tp, size_t smem, int grid,
     if constexpr (I < kNumMasks) {
         if (which != I) return launch_mask<TIn, TOut, INV, V, NT, CL, I + 1, FUSED>(which, tp, smem, grid, stream);
         if constexpr ((V == 1 && !has_row_major_kernel(kMasks[I])) ||
-                      (CL == 2 && (V != 4 || !has_slab_kernel(kMasks[I]) || std::is_same<TOut, int8_t>::value))) {
+                      (CL == 2 && (V != 4 || !has_slab_kernel(kMasks[I]) || is_code<TOut>))) {
             return cudaErrorInvalidValue;
         } else {
             auto kern = harp_tiled_kernel<TIn, TOut, INV, kMasks[I], V, NT, CL, FUSED>;
@@ -958,6 +987,8 @@ cudaError_t harp_tiled_launch_f32(int which, int V, int nt, int cl, bool inverse
                                   size_t smem, int grid, cudaStream_t stream);
 cudaError_t harp_tiled_launch_bf16_f32(int which, int V, int nt, int cl, bool inverse, const harp_tiled::TiledParams& tp,
                                        size_t smem, int grid, cudaStream_t stream);
-// bf16 rows in, int8 codes and per-block fp32 scales out (the fused quantizer epilogue)
+// bf16 rows in, int8 or e4m3 codes and per-block fp32 scales out (the fused quantizer epilogue)
 cudaError_t harp_tiled_launch_bf16_i8(int which, int V, int nt, int cl, bool inverse, const harp_tiled::TiledParams& tp,
                                       size_t smem, int grid, cudaStream_t stream);
+cudaError_t harp_tiled_launch_bf16_e4m3(int which, int V, int nt, int cl, bool inverse,
+                                        const harp_tiled::TiledParams& tp, size_t smem, int grid, cudaStream_t stream);

@@ -20,10 +20,12 @@
 // The device blocks of stage 0 carry the signs (B_0 diag(S)), so kernel 1 accumulates the
 // gradient of those and kernel 2 multiplies column l by the sign of its coordinate.
 #include <algorithm>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "codes.cuh"
 #include "harp_internal.h"
 
 namespace {
@@ -44,6 +46,9 @@ struct GradParams {
     int rs;                               // row stride of the shared-memory tiles (floats)
     int64_t ntiles;
     int vec;                              // rows of x and g load as 16-byte vectors
+    const float* xs;                      // x as 8-bit codes: one scale per qblock coordinates of a row
+    int64_t ld_xs;
+    int qblock;
 };
 
 // Coordinate i of a row sits at swz(i) in shared memory: bits 0-2 of i XOR bits 3-5, bits 3-4
@@ -130,6 +135,58 @@ __device__ void load_tile(const GradParams& p, float* A, float* H, int64_t row0,
                     const int r = q / d, i = q - r * d;
                     A[r * rs + swz(i)] = fx[u];
                     H[r * rs + swz(i)] = fg[u];
+                }
+            }
+        }
+    }
+}
+
+// The same for rows of x that are kept as 8-bit codes of format C: x^ = code * scale, rounded to
+// fp32.  A thread takes 8 coordinates (one scale) of a row at a time; vec: 8-byte loads of codes and
+// 16-byte loads of g.
+template <typename C, typename T>
+__device__ void load_tile_codes(const GradParams& p, float* A, float* H, int64_t row0, int nr) {
+    const int d = (int)p.pd.d, rs = p.rs;
+    const uint8_t* x = (const uint8_t*)p.x;
+    const T* g = (const T*)p.g;
+    constexpr int U = 4;                // groups of 8 in flight per thread
+    const int cpr = (d + 7) / 8, total = nr * cpr;
+    for (int q0 = threadIdx.x; q0 < total; q0 += kThreads * U) {
+        uint2 code[U];
+        float s[U], fg[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int q = q0 + u * kThreads;
+            if (q < total) {
+                const int r = q / cpr, c = 8 * (q - r * cpr), n = min(8, d - c);
+                const uint8_t* src = x + (row0 + r) * p.ld_x + c;
+                if (p.vec && n == 8) {
+                    code[u] = __ldg(reinterpret_cast<const uint2*>(src));
+                } else {
+                    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < n) w[k >> 2] |= (uint32_t)src[k] << (8 * (k & 3));
+                    code[u] = make_uint2(w[0], w[1]);
+                }
+                s[u] = __ldg(p.xs + (row0 + r) * p.ld_xs + c / p.qblock);
+                harp_codes::load8(g + (row0 + r) * p.ld_g + c, n, p.vec, fg[u]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int q = q0 + u * kThreads;
+            if (q < total) {
+                const int r = q / cpr, c = 8 * (q - r * cpr), n = min(8, d - c);
+                float lo[4], hi[4];
+                C::decode4(code[u].x, lo);
+                C::decode4(code[u].y, hi);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (k < n) {
+                        A[r * rs + swz(c + k)] = (k < 4 ? lo[k & 3] : hi[k & 3]) * s[u];
+                        H[r * rs + swz(c + k)] = fg[u][k];
+                    }
                 }
             }
         }
@@ -256,7 +313,8 @@ __device__ void run_stage(const GradParams& p, int t, float* A, float* H, int nr
     __syncthreads();
 }
 
-template <typename T>
+// C: void for rows of x in the type of g, else the format of their 8-bit codes.
+template <typename T, typename C = void>
 __global__ void __launch_bounds__(kThreads, 1) harp_grad_blocks_kernel(const __grid_constant__ GradParams p) {
     extern __shared__ __align__(16) float smem[];
     float* A = smem;                   // activations [row][swz(i)]
@@ -265,7 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1) harp_grad_blocks_kernel(const __g
     for (int64_t tile = blockIdx.x; tile < p.ntiles; tile += gridDim.x) {
         const int64_t row0 = tile * p.R;
         const int nr = (int)min((int64_t)p.R, p.rows - row0);
-        load_tile<T>(p, A, H, row0, nr);
+        if constexpr (std::is_void<C>::value) load_tile<T>(p, A, H, row0, nr);
+        else load_tile_codes<C, T>(p, A, H, row0, nr);
         __syncthreads();
         for (int t = 0; t < m; ++t) run_stage<true>(p, t, A, H, nr);
         for (int t = m - 1; t >= 0; --t) run_stage<false>(p, t, A, H, nr);
@@ -398,10 +457,34 @@ extern "C" size_t harp_grad_workspace_bytes(harp_plan_t p) {
     return acc_layout(p->desc).bytes;
 }
 
-extern "C" harp_status harp_grad_theta(harp_plan_t p, const void* x, const void* g, int64_t rows, int64_t ld_x,
-                                       int64_t ld_g, harp_dtype dtype, float* dtheta, void* workspace,
-                                       size_t ws_bytes, void* stream) {
-    harp_clear_error();
+namespace {
+
+// Rows of x as 8-bit codes; scales == NULL: rows of x in the type of g.
+struct CodedRows {
+    harp_code code;
+    const float* scales;
+    int64_t ld_s;
+    int qblock;
+};
+
+template <typename T, typename C>
+cudaError_t launch_blocks(const GradParams& gp, int grid, size_t smem, cudaStream_t s) {
+    const cudaError_t e = (cudaError_t)harp_set_smem_limit((const void*)harp_grad_blocks_kernel<T, C>, (int)smem);
+    if (e != cudaSuccess) return e;
+    harp_grad_blocks_kernel<T, C><<<grid, kThreads, smem, s>>>(gp);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_blocks(const GradParams& gp, const CodedRows& cr, int grid, size_t smem, cudaStream_t s) {
+    if (!cr.scales) return launch_blocks<T, void>(gp, grid, smem, s);
+    return cr.code == HARP_CODE_I8 ? launch_blocks<T, harp_codes::CodeI8>(gp, grid, smem, s)
+                                   : launch_blocks<T, harp_codes::CodeE4M3>(gp, grid, smem, s);
+}
+
+harp_status grad_checked(harp_plan_t p, const void* x, const void* g, int64_t rows, int64_t ld_x, int64_t ld_g,
+                         harp_dtype dtype, const CodedRows& cr, bool coded, float* dtheta, void* workspace,
+                         size_t ws_bytes, void* stream) {
     if (!p) return harp_fail(HARP_ERR_INVALID_ARG, "plan is NULL");
     if (dtype != HARP_F32 && dtype != HARP_BF16) return harp_fail(HARP_ERR_UNSUPPORTED, "unknown dtype");
     if (rows < 0) return harp_fail(HARP_ERR_INVALID_ARG, "rows < 0");
@@ -427,11 +510,12 @@ extern "C" harp_status harp_grad_theta(harp_plan_t p, const void* x, const void*
         return harp_fail(HARP_ERR_INVALID_ARG, "workspace smaller than harp_grad_workspace_bytes()");
     if (((uintptr_t)workspace & 15) != 0) return harp_fail(HARP_ERR_INVALID_ARG, "workspace not 16-byte aligned");
     if (rows > 0 && (!x || !g)) return harp_fail(HARP_ERR_INVALID_ARG, "x or g is NULL");
+    if (rows > 0 && coded && !cr.scales) return harp_fail(HARP_ERR_INVALID_ARG, "the codes' scales are NULL");
     {
         // the accumulators are zeroed and then added to while x and g are read, and dtheta is
         // written last: none of them may share memory with another
         const size_t es = dtype == HARP_F32 ? 4 : 2;
-        const size_t xb = rows > 0 ? ((size_t)(rows - 1) * ld_x + d) * es : 0;
+        const size_t xb = rows > 0 ? ((size_t)(rows - 1) * ld_x + d) * (coded ? 1 : es) : 0;
         const size_t gb = rows > 0 ? ((size_t)(rows - 1) * ld_g + d) * es : 0;
         const size_t tb = (size_t)p->theta_total * sizeof(float);
         if (rows > 0 && (ranges_overlap(workspace, ws_bytes, x, xb) || ranges_overlap(workspace, ws_bytes, g, gb)))
@@ -439,6 +523,11 @@ extern "C" harp_status harp_grad_theta(harp_plan_t p, const void* x, const void*
         if (ranges_overlap(dtheta, tb, workspace, ws_bytes) ||
             (rows > 0 && (ranges_overlap(dtheta, tb, x, xb) || ranges_overlap(dtheta, tb, g, gb))))
             return harp_fail(HARP_ERR_INVALID_ARG, "dtheta overlaps the workspace, x or g");
+        if (rows > 0 && coded) {
+            const size_t sb = ((size_t)(rows - 1) * cr.ld_s + (d + cr.qblock - 1) / cr.qblock) * sizeof(float);
+            if (ranges_overlap(workspace, ws_bytes, cr.scales, sb) || ranges_overlap(dtheta, tb, cr.scales, sb))
+                return harp_fail(HARP_ERR_INVALID_ARG, "dtheta or the workspace overlaps the scales");
+        }
     }
     // rows per tile: two fp32 tiles of rows rounded up to 32 coordinates (the swizzle
     // permutes aligned blocks of 32) within the 227 KiB of shared memory a CTA may use
@@ -467,18 +556,16 @@ extern "C" harp_status harp_grad_theta(harp_plan_t p, const void* x, const void*
         gp.rs = rs;
         gp.ntiles = (rows + R - 1) / R;
         const size_t es = dtype == HARP_F32 ? 4 : 2;
-        gp.vec = ((uintptr_t)x % 16 == 0) && ((uintptr_t)g % 16 == 0) && (ld_x * es) % 16 == 0 &&
-                 (ld_g * es) % 16 == 0 && (d * es) % 16 == 0;
+        gp.xs = cr.scales, gp.ld_xs = cr.ld_s, gp.qblock = cr.qblock;
+        if (coded)
+            gp.vec = ((uintptr_t)x % 8 == 0) && ((uintptr_t)g % 16 == 0) && ld_x % 8 == 0 && (ld_g * es) % 16 == 0;
+        else
+            gp.vec = ((uintptr_t)x % 16 == 0) && ((uintptr_t)g % 16 == 0) && (ld_x * es) % 16 == 0 &&
+                     (ld_g * es) % 16 == 0 && (d * es) % 16 == 0;
         const size_t smem = (size_t)R * per_row;
         const int grid = (int)std::min<int64_t>(gp.ntiles, sms_of_current_device());
-        if (dtype == HARP_BF16) {
-            e = (cudaError_t)harp_set_smem_limit((const void*)harp_grad_blocks_kernel<__nv_bfloat16>, (int)smem);
-            if (e == cudaSuccess) harp_grad_blocks_kernel<__nv_bfloat16><<<grid, kThreads, smem, s>>>(gp);
-        } else {
-            e = (cudaError_t)harp_set_smem_limit((const void*)harp_grad_blocks_kernel<float>, (int)smem);
-            if (e == cudaSuccess) harp_grad_blocks_kernel<float><<<grid, kThreads, smem, s>>>(gp);
-        }
-        if (e == cudaSuccess) e = cudaGetLastError();
+        e = dtype == HARP_BF16 ? launch_blocks<__nv_bfloat16>(gp, cr, grid, smem, s)
+                               : launch_blocks<float>(gp, cr, grid, smem, s);
         if (e != cudaSuccess) return harp_fail(HARP_ERR_CUDA, cudaGetErrorString(e));
     }
     int64_t total = 0;
@@ -491,4 +578,31 @@ extern "C" harp_status harp_grad_theta(harp_plan_t p, const void* x, const void*
     if (e != cudaSuccess) return harp_fail(HARP_ERR_CUDA, cudaGetErrorString(e));
     harp_set_last_kernel("harp_grad_blocks_kernel");
     return HARP_OK;
+}
+
+}  // namespace
+
+extern "C" harp_status harp_grad_theta(harp_plan_t p, const void* x, const void* g, int64_t rows, int64_t ld_x,
+                                       int64_t ld_g, harp_dtype dtype, float* dtheta, void* workspace,
+                                       size_t ws_bytes, void* stream) {
+    harp_clear_error();
+    return grad_checked(p, x, g, rows, ld_x, ld_g, dtype, CodedRows{HARP_CODE_I8, nullptr, 0, 1}, false, dtheta,
+                        workspace, ws_bytes, stream);
+}
+
+extern "C" harp_status harp_grad_theta_quant(harp_plan_t p, const void* q, int64_t ld_q, harp_code code,
+                                             const float* scales, int64_t ld_s, int32_t qblock, const void* g,
+                                             int64_t ld_g, harp_dtype dtype, int64_t rows, float* dtheta,
+                                             void* workspace, size_t ws_bytes, void* stream) {
+    harp_clear_error();
+    if (!p) return harp_fail(HARP_ERR_INVALID_ARG, "plan is NULL");
+    if (code != HARP_CODE_I8 && code != HARP_CODE_E4M3) return harp_fail(HARP_ERR_UNSUPPORTED, "unknown code format");
+    if (qblock != 32 && qblock != 64 && qblock != 128 && qblock != 256)
+        return harp_fail(HARP_ERR_INVALID_ARG, "qblock must be 32, 64, 128 or 256");
+    if (ld_s < (p->desc.d + qblock - 1) / qblock)
+        return harp_fail(HARP_ERR_INVALID_ARG, "leading dimension smaller than the row");
+    if ((uintptr_t)scales % 4 || (uintptr_t)g % (dtype == HARP_F32 ? 4 : 2))
+        return harp_fail(HARP_ERR_INVALID_ARG, "a pointer is not aligned to its element type");
+    return grad_checked(p, q, g, rows, ld_q, ld_g, dtype, CodedRows{code, scales, ld_s, qblock}, true, dtheta,
+                        workspace, ws_bytes, stream);
 }

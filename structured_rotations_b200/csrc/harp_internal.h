@@ -77,6 +77,8 @@ void harp_set_last_kernel(const char* name);
 // to at least `bytes` on the current device; the runtime call is made only the first time a
 // kernel needs more than before, since it costs microseconds on every launch otherwise.
 int harp_set_smem_limit(const void* kernel, int bytes);
+// SMs of the current device (api.cu)
+int harp_sm_count();
 
 // device helpers (materialize.cu)
 harp_status harp_device_free(harp_plan_s* p);
@@ -115,9 +117,9 @@ harp_status launch_apply_cluster(const harp_plan_s* p, const void* x, void* y, i
 // cluster fits, no tensor-map encoder) is left without one and runs on the other kernels.
 // The specialized kernel with the blockwise quantizer as its epilogue (harp_apply_quant on a
 // d = 4096 (8,8,8,8) plan, forward); HARP_ERR_UNSUPPORTED for anything else.
-harp_status launch_apply_fast_quant(harp_plan_s* p, const void* x, int64_t rows, int64_t ld_x, int8_t* q,
-                                    int64_t ld_q, float* scales, int64_t ld_s, int qblock, harp_dir dir,
-                                    void* stream);
+harp_status launch_apply_fast_quant(harp_plan_s* p, const void* x, int64_t rows, int64_t ld_x, void* q,
+                                    int64_t ld_q, float* scales, int64_t ld_s, int qblock, harp_code code,
+                                    harp_dir dir, void* stream);
 void fast_prepare(harp_plan_s* p, void* stream);
 void host_io_free(harp_plan_s* p);
 
@@ -131,12 +133,13 @@ harp_status run_rows(harp_plan_s* p, const void* x, void* y, int64_t rows, int64
 harp_status launch_cols(const harp_plan_s* p, float* x, int64_t ld_x, int64_t ncols, void* y, int64_t ld_y,
                         harp_dtype out_dtype, harp_dir dir, void* stream);
 
-// Int8 output of the tiled kernel (the fused quantizer epilogue): y receives int8 codes,
+// 8-bit output of the tiled kernel (the fused quantizer epilogue): y receives the codes,
 // `scales` one fp32 scale per block of `qblock` coordinates (row stride ld_s floats).
 struct QuantOut {
     float* scales;
     int64_t ld_s;
     int qblock;
+    harp_code code;
 };
 
 // General tiled row kernel (apply_tiled.cu): radices 2..8, d % 8 == 0, 16-byte aligned

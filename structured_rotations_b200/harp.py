@@ -29,6 +29,8 @@ HARP_THETA_F32 = 0
 HARP_THETA_I8 = 1
 HARP_F32 = 0
 HARP_BF16 = 1
+HARP_CODE_I8 = 0
+HARP_CODE_E4M3 = 1
 HARP_FORWARD = 0
 HARP_INVERSE = 1
 
@@ -77,6 +79,18 @@ def lib():
         "harp_plan_compose": (_c_i32, [ctypes.POINTER(_vp), ctypes.POINTER(_vp), _c_i32, _vp]),
         "harp_apply_quant": (_c_i32, [_vp, _vp, _c_i64, _c_i64, _c_i32, _vp, _c_i64, _vp, _c_i64, _c_i32, _c_i32,
                                       _vp]),
+        "harp_apply_quant_ex": (_c_i32, [_vp, _vp, _c_i64, _c_i64, _c_i32, _c_i32, _vp, _c_i64, _vp, _c_i64, _c_i32,
+                                         _c_i32, _vp]),
+        "harp_quantize": (_c_i32, [_vp, _c_i64, _c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _c_i32, _vp, _c_i64, _vp,
+                                   _c_i64, _vp]),
+        "harp_dequantize": (_c_i32, [_vp, _c_i64, _vp, _c_i64, _c_i32, _c_i32, _c_i32, _c_i64, _c_i64, _vp, _c_i64,
+                                     _c_i32, _vp]),
+        "harp_rms_norm_quant": (_c_i32, [_vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _c_i64, _c_i32, ctypes.c_double, _vp,
+                                         _c_i64, _vp, _c_i64, _c_i32, _c_i32, _vp, _c_i64, _vp, _c_i64, _vp]),
+        "harp_matmul_quant": (_c_i32, [_vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _c_i64, _c_i64, _c_i64,
+                                       _vp, _c_i64, _c_i32, _vp]),
+        "harp_grad_theta_quant": (_c_i32, [_vp, _vp, _c_i64, _c_i32, _vp, _c_i64, _c_i32, _vp, _c_i64, _c_i32, _c_i64,
+                                           _vp, _vp, ctypes.c_size_t, _vp]),
         "harp_grad_theta": (_c_i32, [_vp, _vp, _vp, _c_i64, _c_i64, _c_i64, _c_i32, _vp, _vp, ctypes.c_size_t,
                                      _vp]),
         "harp_off_block_energy": (_c_i32, [_vp, _c_i64, _c_i64, _c_i32, _c_i32, _vp, _vp]),
@@ -163,6 +177,45 @@ def _ld(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
+_CODE = {"int8": HARP_CODE_I8, "e4m3": HARP_CODE_E4M3}
+
+
+def _code(name: str) -> int:
+    if name not in _CODE:
+        raise ValueError(f"code must be 'int8' or 'e4m3', not {name!r}")
+    return _CODE[name]
+
+
+def _code_dtype(code: int):
+    import torch
+    return torch.int8 if code == HARP_CODE_I8 else torch.float8_e4m3fn
+
+
+def _code_of(q) -> int:
+    """The code format of a tensor of codes, by its type."""
+    import torch
+    if q.dtype == torch.int8:
+        return HARP_CODE_I8
+    if q.dtype == torch.float8_e4m3fn:
+        return HARP_CODE_E4M3
+    raise TypeError(f"codes are int8 or float8_e4m3fn tensors, not {q.dtype}")
+
+
+def _expect(t, shape, dtype, what: str):
+    """t is a CUDA tensor of the current device with this shape and type and contiguous rows."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    import torch
+    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{what} must be on the current CUDA device, not {t.device}")
+
+
+def _cdiv(a: int, b: int) -> int:
+    return -(-a // b)
+
+
 class Plan:
     """One HARP rotation: schedule, parameters, signs, mixers and device blocks."""
 
@@ -233,23 +286,73 @@ class Plan:
                                 _dtype_code(x), d, _stream_handle(stream)), "harp_apply")
         return y
 
-    def apply_quant(self, x, qblock: int = 128, direction: str = "forward", q=None, scales=None, stream=None):
-        """T x (or T^T x) with the fused blockwise quantizer (harp_apply_quant): bf16 rows in,
-        int8 codes [rows, d] and float32 scales [rows, d / qblock] out, y ~= q * scale per
-        aligned block of qblock coordinates.  Returns (q, scales)."""
+    def apply_quant(self, x, qblock: int = 128, direction: str = "forward", q=None, scales=None, stream=None,
+                    code: str = "int8"):
+        """T x (or T^T x) with the fused blockwise quantizer (harp_apply_quant_ex): bf16 rows in,
+        codes [rows, d] (int8, or float8_e4m3fn for code="e4m3") and float32 scales
+        [rows, d / qblock] out, y ~= q * scale per aligned block of qblock coordinates.
+        Returns (q, scales); e4m3 codes in blocks of 128 are matmul_quant's row operand."""
         import torch
         if x.shape[-1] != self.d:
             raise ValueError(f"last dimension must be d={self.d}")
+        fmt = _code(code)
         rows = x.shape[0]
         if q is None:
-            q = torch.empty(rows, self.d, dtype=torch.int8, device=x.device)
+            q = torch.empty(rows, self.d, dtype=_code_dtype(fmt), device=x.device)
         if scales is None:
             scales = torch.empty(rows, max(1, self.d // qblock), dtype=torch.float32, device=x.device)
+        if code == "e4m3":
+            _expect(x, (rows, self.d), x.dtype, "x")
+            _expect(q, (rows, self.d), torch.float8_e4m3fn, "q")
+            _expect(scales, (rows, max(1, self.d // qblock)), torch.float32, "scales")
         d = HARP_FORWARD if direction == "forward" else HARP_INVERSE
-        _check(lib().harp_apply_quant(self._h, x.data_ptr(), rows, _ld(x), _dtype_code(x), q.data_ptr(), _ld(q),
-                                      scales.data_ptr(), _ld(scales), qblock, d, _stream_handle(stream)),
+        _check(lib().harp_apply_quant_ex(self._h, x.data_ptr(), rows, _ld(x), _dtype_code(x), fmt, q.data_ptr(),
+                                         _ld(q), scales.data_ptr(), _ld(scales), qblock, d, _stream_handle(stream)),
                "harp_apply_quant")
         return q, scales
+
+    def grad_workspace(self, device=None):
+        """A workspace for grad_theta and grad_theta_quant (uint8, harp_grad_workspace_bytes), to keep
+        between calls; calls that may run at once need one each."""
+        import torch
+        return torch.empty(int(lib().harp_grad_workspace_bytes(self._h)), dtype=torch.uint8,
+                           device="cuda" if device is None else device)
+
+    def grad_theta_quant(self, q, scales, g, dtheta=None, workspace=None, stream=None, qblock: Optional[int] = None):
+        """dL/dtheta for L = sum_r g_r . (T x_r) with the rows x kept as 8-bit checkpoints
+        (harp_grad_theta_quant): codes q [rows, d] (int8 or float8_e4m3fn) and float32 scales
+        [rows, ceil(d / qblock)] of H.quantize(x, (1, qblock), ...), upstream gradients g [rows, d]
+        (bf16 or fp32).  qblock defaults to the one that the scales' shape gives when it divides d.
+        Returns a float32 tensor of theta_count entries."""
+        import torch
+        rows = q.shape[0]
+        if qblock is None:
+            nb = scales.shape[1] if scales.dim() == 2 else 0
+            if nb < 1 or self.d % nb or self.d // nb not in (32, 64, 128, 256):
+                raise ValueError("give qblock: the scales' shape does not tell it")
+            qblock = self.d // nb
+        if qblock not in (32, 64, 128, 256):
+            raise ValueError("qblock must be 32, 64, 128 or 256")
+        code = _code_of(q)
+        _expect(q, (rows, self.d), q.dtype, "q")
+        _expect(scales, (rows, _cdiv(self.d, qblock)), torch.float32, "scales")
+        gt = _dtype_code(g)
+        _expect(g, (rows, self.d), g.dtype, "g")
+        n = theta_count(self.schedule) if not getattr(self, "composite", False) else 1
+        if dtheta is None:
+            dtheta = torch.empty(n, dtype=torch.float32, device=q.device)
+        elif not dtheta.is_contiguous():
+            raise ValueError(f"dtheta must be a contiguous float32 tensor of {n} entries")
+        _expect(dtheta, (n,), torch.float32, "dtheta")
+        if workspace is None:
+            workspace = self.grad_workspace(q.device)
+        elif not workspace.is_contiguous() or not workspace.is_cuda or workspace.device != q.device:
+            raise ValueError("workspace must be contiguous, on the rows' device")
+        _check(lib().harp_grad_theta_quant(self._h, q.data_ptr(), _ld(q), code, scales.data_ptr(), _ld(scales), qblock,
+                                           g.data_ptr(), _ld(g), gt, rows, dtheta.data_ptr(), workspace.data_ptr(),
+                                           workspace.numel() * workspace.element_size(), _stream_handle(stream)),
+               "harp_grad_theta_quant")
+        return dtheta
 
     def grad_theta(self, x, g, dtheta=None, workspace=None, stream=None):
         """dL/dtheta for L = sum_r g_r . (T x_r) (harp_grad_theta): the calibration backward
@@ -429,3 +532,125 @@ def moment_check(x, tau1: float = 0.0, tau2: float = 0.0, moments=None, passes=N
                                    moments.data_ptr(), passes.data_ptr(), _stream_handle(stream)),
            "harp_moment_check")
     return moments, passes
+
+
+def quantize(x, block=(1, 128), code: str = "e4m3", q=None, scales=None, stream=None):
+    """8-bit codes of the device matrix x with one float32 scale per block (harp_quantize):
+    x ~= q * scale, q int8 or float8_e4m3fn [rows, cols], scales [ceil(rows / b0), ceil(cols / b1)]
+    for block = (b0, b1): (1, 32 | 64 | 128 | 256) for rows (checkpoints for Plan.grad_theta_quant;
+    e4m3 with 128: matmul_quant's row operand), (128, 128) for a weight (matmul_quant's).
+    Returns (q, scales).  A new q has rows a multiple of 16 bytes apart."""
+    import torch
+    fmt = _code(code)
+    if x.dim() != 2:
+        raise ValueError("expected a 2-D tensor of rows")
+    rows, cols = x.shape
+    dt = _dtype_code(x)
+    _expect(x, (rows, cols), x.dtype, "x")
+    br, bc = int(block[0]), int(block[1])
+    if br < 1 or bc < 1:
+        raise ValueError("blocks are (1, 32 | 64 | 128 | 256) or (128, 128)")
+    if q is None:
+        q = torch.empty(rows, _cdiv(cols, 16) * 16, dtype=_code_dtype(fmt), device=x.device)[:, :cols]
+    if scales is None:
+        scales = torch.empty(_cdiv(rows, br), _cdiv(cols, bc), dtype=torch.float32, device=x.device)
+    _expect(q, (rows, cols), _code_dtype(fmt), "q")
+    _expect(scales, (_cdiv(rows, br), _cdiv(cols, bc)), torch.float32, "scales")
+    _check(lib().harp_quantize(x.data_ptr(), rows, cols, _ld(x), dt, fmt, br, bc, q.data_ptr(), _ld(q),
+                               scales.data_ptr(), _ld(scales), _stream_handle(stream)), "harp_quantize")
+    return q, scales
+
+
+def dequantize(q, scales, block=(1, 128), out=None, dtype=None, stream=None):
+    """The values q * scale of quantize's codes (harp_dequantize), rounded to out's type (a new tensor
+    of `dtype`, bfloat16 by default).  Returns out."""
+    import torch
+    code = _code_of(q)
+    if q.dim() != 2:
+        raise ValueError("expected a 2-D tensor of codes")
+    rows, cols = q.shape
+    br, bc = int(block[0]), int(block[1])
+    if br < 1 or bc < 1:
+        raise ValueError("blocks are (1, 32 | 64 | 128 | 256) or (128, 128)")
+    if out is None:
+        out = torch.empty(rows, cols, dtype=dtype or torch.bfloat16, device=q.device)
+    elif dtype is not None and out.dtype != dtype:
+        raise TypeError("out has another dtype")
+    dt = _dtype_code(out)
+    _expect(q, (rows, cols), q.dtype, "q")
+    _expect(scales, (_cdiv(rows, br), _cdiv(cols, bc)), torch.float32, "scales")
+    _expect(out, (rows, cols), out.dtype, "out")
+    _check(lib().harp_dequantize(q.data_ptr(), _ld(q), scales.data_ptr(), _ld(scales), code, br, bc, rows, cols,
+                                 out.data_ptr(), _ld(out), dt, _stream_handle(stream)), "harp_dequantize")
+    return out
+
+
+def rms_norm_quant(x, weight=None, residual=None, eps: float = 1e-6, qblock: int = 128, code: str = "e4m3", h=None,
+                   y=None, q=None, scales=None, stream=None):
+    """h = x + residual, u = h / sqrt(mean(h^2) + eps) * weight and u's 8-bit codes in one pass
+    (harp_rms_norm_quant).  x and residual: rows [rows, d] (bf16 or fp32), weight [d] of their type or
+    None.  h receives the sum (it may be x or residual; a new tensor where there is a residual),
+    y, if given, u rounded to x's type.  Returns (q, scales, h): codes [rows, d] (int8 or
+    float8_e4m3fn), float32 scales [rows, ceil(d / qblock)], and the sum (x itself without a
+    residual, unless h is given)."""
+    import torch
+    fmt = _code(code)
+    if x.dim() != 2:
+        raise ValueError("expected a 2-D tensor of rows")
+    rows, d = x.shape
+    dt = _dtype_code(x)
+    if qblock not in (32, 64, 128, 256):
+        raise ValueError("qblock must be 32, 64, 128 or 256")
+    _expect(x, (rows, d), x.dtype, "x")
+    if residual is not None:
+        _expect(residual, (rows, d), x.dtype, "residual")
+        if h is None:
+            h = torch.empty(rows, d, dtype=x.dtype, device=x.device)
+    if weight is not None:
+        _expect(weight, (d,), x.dtype, "weight")
+        if d > 1 and weight.stride(0) != 1:
+            raise ValueError("weight must be contiguous")
+    if h is not None:
+        _expect(h, (rows, d), x.dtype, "h")
+    if y is not None:
+        _expect(y, (rows, d), x.dtype, "y")
+    if q is None:
+        q = torch.empty(rows, _cdiv(d, 16) * 16, dtype=_code_dtype(fmt), device=x.device)[:, :d]
+    if scales is None:
+        scales = torch.empty(rows, _cdiv(d, qblock), dtype=torch.float32, device=x.device)
+    _expect(q, (rows, d), _code_dtype(fmt), "q")
+    _expect(scales, (rows, _cdiv(d, qblock)), torch.float32, "scales")
+    _check(lib().harp_rms_norm_quant(
+        x.data_ptr(), _ld(x), None if residual is None else residual.data_ptr(), 0 if residual is None else _ld(residual),
+        None if weight is None else weight.data_ptr(), rows, d, dt, float(eps), None if h is None else h.data_ptr(),
+        0 if h is None else _ld(h), None if y is None else y.data_ptr(), 0 if y is None else _ld(y), fmt, qblock,
+        q.data_ptr(), _ld(q), scales.data_ptr(), _ld(scales), _stream_handle(stream)), "harp_rms_norm_quant")
+    return q, scales, x if h is None else h
+
+
+def matmul_quant(xq, xs, wq, ws, out=None, dtype=None, stream=None):
+    """out = (xq * xs) (wq * ws)^T (harp_matmul_quant): e4m3 codes xq [rows, k] with float32 scales
+    xs [rows, ceil(k / 128)], e4m3 codes wq [n, k] with scales ws [ceil(n / 128), ceil(k / 128)];
+    out [rows, n] in bfloat16 (the default) or float32.  Operands 16-byte aligned with leading
+    dimensions that are multiples of 16, as quantize and apply_quant make them, run on the tensor
+    cores.  Returns out."""
+    import torch
+    if xq.dim() != 2 or wq.dim() != 2:
+        raise ValueError("expected 2-D tensors of codes")
+    rows, k = xq.shape
+    n = wq.shape[0]
+    f8 = torch.float8_e4m3fn
+    _expect(xq, (rows, k), f8, "xq")
+    _expect(wq, (n, k), f8, "wq")
+    _expect(xs, (rows, _cdiv(k, 128)), torch.float32, "xs")
+    _expect(ws, (_cdiv(n, 128), _cdiv(k, 128)), torch.float32, "ws")
+    if out is None:
+        out = torch.empty(rows, n, dtype=dtype or torch.bfloat16, device=xq.device)
+    elif dtype is not None and out.dtype != dtype:
+        raise TypeError("out has another dtype")
+    dt = _dtype_code(out)
+    _expect(out, (rows, n), out.dtype, "out")
+    _check(lib().harp_matmul_quant(xq.data_ptr(), _ld(xq), xs.data_ptr(), _ld(xs), wq.data_ptr(), _ld(wq),
+                                   ws.data_ptr(), _ld(ws), rows, n, k, out.data_ptr(), _ld(out), dt,
+                                   _stream_handle(stream)), "harp_matmul_quant")
+    return out
