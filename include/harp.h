@@ -493,6 +493,11 @@ HARP_API harp_status harp_plan_compose(harp_plan_t* out, const harp_plan_t* plan
  * not, HARP_ERR_NOT_MATERIALIZED before materialization. */
 HARP_API harp_status harp_plan_device_status(harp_plan_t plan);
 
+/* harp_device_status — the same for the entry points without a plan (harp_matmul_quant) on
+ * the current device: synchronizes it and returns HARP_ERR_TIMEOUT if a bounded wait gave up since
+ * the last call (the result of that call is then not valid). */
+HARP_API harp_status harp_device_status(void);
+
 /* harp_plan_destroy — free the plan and its device memory (synchronizes the
  * device that owns it).  NULL is accepted. */
 HARP_API harp_status harp_plan_destroy(harp_plan_t plan);

@@ -4,10 +4,15 @@
 // matmul_simple_kernel takes any alignment: a CTA computes 64 x 64 results, the codes of a
 // 32-wide slice of k decoded to fp32 in shared memory, each thread 4 x 4 fp32 sums per block of
 // 128, which are scaled and added up in fp32 at the block's end.
+// matmul_rows.cu holds the tensor-core kernel for few rows.
 #include <algorithm>
+#include <atomic>
+#include <mutex>
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include "codes.cuh"
 #include "harp_internal.h"
@@ -93,7 +98,79 @@ harp_status launch_simple(const MatmulParams& p, harp_dtype out, cudaStream_t st
     return HARP_OK;
 }
 
+// set by a bounded wait that gave up (harp_device_status)
+__device__ int g_wait_status;
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static std::once_flag once;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult res;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &res) == cudaSuccess &&
+            res == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+        cudaGetLastError();
+    });
+    return fn;
+}
+
 }  // namespace
+
+harp_status matmul_tensor_map(CUtensorMap* map, const void* q, int64_t rows, int64_t k, int64_t ld, int box_rows) {
+    auto encode = encoder();
+    if (!encode) return harp_fail(HARP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    const cuuint64_t dim[2] = {(cuuint64_t)k, (cuuint64_t)rows};
+    const cuuint64_t stride[1] = {(cuuint64_t)ld};
+    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    const cuuint32_t step[2] = {1, 1};
+    auto run = [&] {
+        return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(q), dim, stride, box, step,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = run();
+    if (r == CUDA_ERROR_INVALID_CONTEXT) {
+        // a host thread whose first CUDA call this is has no current context yet
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) cudaGetLastError();
+        r = run();
+    }
+    if (r != CUDA_SUCCESS) return harp_fail(HARP_ERR_CUDA, "cuTensorMapEncodeTiled failed: " + std::to_string((int)r));
+    return HARP_OK;
+}
+
+int* matmul_status_word() {
+    static std::atomic<int*> cached[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        cudaGetLastError();
+        return nullptr;
+    }
+    int* p = cached[dev].load(std::memory_order_relaxed);
+    if (!p) {
+        void* a = nullptr;
+        if (cudaGetSymbolAddress(&a, g_wait_status) != cudaSuccess) {
+            cudaGetLastError();
+            return nullptr;
+        }
+        p = (int*)a;
+        cached[dev].store(p, std::memory_order_relaxed);
+    }
+    return p;
+}
+
+extern "C" harp_status harp_device_status(void) {
+    harp_clear_error();
+    int* word = matmul_status_word();
+    if (!word) return harp_fail(HARP_ERR_CUDA, "no CUDA device");
+    int v = 0;
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) e = cudaMemcpy(&v, word, sizeof v, cudaMemcpyDeviceToHost);
+    if (e == cudaSuccess && v) e = cudaMemset(word, 0, sizeof v);
+    if (e != cudaSuccess) return harp_fail(HARP_ERR_CUDA, cudaGetErrorString(e));
+    return v ? harp_fail(HARP_ERR_TIMEOUT, "a bounded device-side wait gave up") : HARP_OK;
+}
 
 extern "C" harp_status harp_matmul_quant(const void* x, int64_t ld_x, const float* sx, int64_t ld_sx, const void* w,
                                          int64_t ld_w, const float* sw, int64_t ld_sw, int64_t rows, int64_t n,
@@ -117,5 +194,13 @@ extern "C" harp_status harp_matmul_quant(const void* x, int64_t ld_x, const floa
         ranges_overlap(y, yb, sw, ((size_t)(nb - 1) * ld_sw + kb) * 4))
         return harp_fail(HARP_ERR_INVALID_ARG, "the result overlaps an operand");
     const MatmulParams p{(const uint8_t*)x, (const uint8_t*)w, sx, sw, y, ld_x, ld_w, ld_sx, ld_sw, ld_y, rows, n, k, kb};
+    // TMA takes 16-byte aligned operands whose rows are a multiple of 16 bytes (below 2^40) apart
+    const bool tma = ((uintptr_t)x | (uintptr_t)w | (uintptr_t)ld_x | (uintptr_t)ld_w) % 16 == 0 && ld_x < (1ll << 40) &&
+                     ld_w < (1ll << 40);
+    if (tma) {
+        const harp_status st = launch_matmul_rows(p, out_dtype, stream);
+        if (st != HARP_ERR_UNSUPPORTED) return st;
+        harp_clear_error();
+    }
     return launch_simple(p, out_dtype, (cudaStream_t)stream);
 }

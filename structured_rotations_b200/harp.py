@@ -75,6 +75,7 @@ def lib():
                                                   _vp]),
         "harp_noalloc_scratch_bytes": (ctypes.c_size_t, []),
         "harp_plan_device_status": (_c_i32, [_vp]),
+        "harp_device_status": (_c_i32, []),
         "harp_grad_workspace_bytes": (ctypes.c_size_t, [_vp]),
         "harp_plan_compose": (_c_i32, [ctypes.POINTER(_vp), ctypes.POINTER(_vp), _c_i32, _vp]),
         "harp_apply_quant": (_c_i32, [_vp, _vp, _c_i64, _c_i64, _c_i32, _vp, _c_i64, _vp, _c_i64, _c_i32, _c_i32,
@@ -654,3 +655,9 @@ def matmul_quant(xq, xs, wq, ws, out=None, dtype=None, stream=None):
                                    ws.data_ptr(), _ld(ws), rows, n, k, out.data_ptr(), _ld(out), dt,
                                    _stream_handle(stream)), "harp_matmul_quant")
     return out
+
+
+def device_status() -> None:
+    """Synchronize the current device and raise HarpError(HARP_ERR_TIMEOUT) if a bounded device wait of
+    matmul_quant gave up since the last call (harp_device_status)."""
+    _check(lib().harp_device_status(), "harp_device_status")

@@ -71,6 +71,7 @@ def test_exact_sums(m, n, k):
     want = _want(xq, xs, wq, ws)
     assert torch.equal(H.matmul_quant(xq, xs, wq, ws, dtype=torch.float32), want.float())
     assert torch.equal(H.matmul_quant(xq, xs, wq, ws), want.float().bfloat16())
+    H.device_status()
 
 
 @pytest.mark.parametrize("m,n,k", SIZES[::2] + [(7, 28672, 8192), (700, 4096, 8192)])
