@@ -198,7 +198,7 @@ extern "C" harp_status harp_matmul_quant(const void* x, int64_t ld_x, const floa
     const bool tma = ((uintptr_t)x | (uintptr_t)w | (uintptr_t)ld_x | (uintptr_t)ld_w) % 16 == 0 && ld_x < (1ll << 40) &&
                      ld_w < (1ll << 40);
     if (tma) {
-        const harp_status st = launch_matmul_rows(p, out_dtype, stream);
+        const harp_status st = rows > 128 ? launch_matmul_tiles(p, out_dtype, stream) : launch_matmul_rows(p, out_dtype, stream);
         if (st != HARP_ERR_UNSUPPORTED) return st;
         harp_clear_error();
     }

@@ -23,3 +23,5 @@ int* matmul_status_word();
 
 // Few rows: 16-byte aligned operands and leading dimensions.
 harp_status launch_matmul_rows(const MatmulParams& p, harp_dtype out, void* stream);
+// Many rows: the same alignment.
+harp_status launch_matmul_tiles(const MatmulParams& p, harp_dtype out, void* stream);

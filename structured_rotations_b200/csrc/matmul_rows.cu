@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
             for (int c0 = 0; c0 < BT; c0 += W) {
                 uint32_t v[W];
                 tmem_ld(addr + c0, v);
-                tmem_ld_wait();
+                tmem_ld_wait(v);
                 if (c0 + W == BT) {
                     fence_before();
                     __syncwarp();
