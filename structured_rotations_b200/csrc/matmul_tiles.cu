@@ -187,13 +187,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             float sum[N];
 #pragma unroll
             for (int c = 0; c < N; ++c) sum[c] = 0.f;
-            float next = row ? __ldg(sx) * __ldg(sw) : 0.f;
+            // scales two blocks ahead of their use
+            float x0 = row ? __ldg(sx) : 0.f, w0 = __ldg(sw), x1 = 0.f, w1 = 0.f;
+            if (kb > 1) x1 = row ? __ldg(sx + 1) : 0.f, w1 = __ldg(sw + 1);
             for (int k = 0; k < kb; ++k) {
-                const float f = next;
-                if (row && k + 1 < kb) next = __ldg(sx + k + 1) * __ldg(sw + k + 1);
+                float x2 = 0.f, w2 = 0.f;
+                if (k + 2 < kb) x2 = row ? __ldg(sx + k + 2) : 0.f, w2 = __ldg(sw + k + 2);
                 ok = __all_sync(0xffffffffu, mbar_wait(tfull + b, bph, failed, status));
                 if (!ok) break;
                 fence_after();
+                const float f = x0 * w0;
+                x0 = x1, w0 = w1, x1 = x2, w1 = w2;
                 const uint32_t addr = tmem + lanes + b * NT + N * half;
                 uint32_t v[2][16];
                 tmem_ld(addr, v[0]);
