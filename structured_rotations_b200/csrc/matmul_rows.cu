@@ -79,30 +79,32 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
     for (int c = 0; c < BT; ++c) sum[c] = 0.f;
 
     if (warp == 4) {
-        if (lane == 0) {
-            for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
-                const int s = i % S::kStages;
-                if (i >= S::kStages && !mbar_wait(empty + s, ((i / S::kStages) & 1) ^ 1, failed, status)) break;
+        for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
+            const int s = i % S::kStages;
+            if (i >= S::kStages && !mbar_wait_warp(empty + s, ((i / S::kStages) & 1) ^ 1, failed, status)) break;
+            if (elect_one()) {
                 unsigned char* st = stages + s * S::kStageBytes;
                 mbar_expect_tx(full + s, S::kStageBytes);
                 tma_load(st, &map_w, kb * 128, (int)n0, full + s);
                 tma_load(st + 128 * 128, &map_x, kb * 128, (int)m0, full + s);
             }
+            __syncwarp();
         }
     } else if (warp == 5) {
-        if (lane == 0) {
-            for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
-                const int s = i % S::kStages, b = i % S::kBuffers;
-                if (!mbar_wait(full + s, (i / S::kStages) & 1, failed, status)) break;
-                if (i >= S::kBuffers && !mbar_wait(tempty + b, ((i / S::kBuffers) & 1) ^ 1, failed, status)) break;
-                fence_after();
-                const uint64_t a = operand_desc(stages + s * S::kStageBytes), bd = operand_desc(stages + s * S::kStageBytes + 128 * 128);
+        for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
+            const int s = i % S::kStages, b = i % S::kBuffers;
+            if (!mbar_wait_warp(full + s, (i / S::kStages) & 1, failed, status)) break;
+            if (i >= S::kBuffers && !mbar_wait_warp(tempty + b, ((i / S::kBuffers) & 1) ^ 1, failed, status)) break;
+            fence_after();
+            const uint64_t a = operand_desc(stages + s * S::kStageBytes);
+            const uint64_t bd = operand_desc(stages + s * S::kStageBytes + 128 * 128);
+            if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma<1>(tmem + b * BT, a + 2 * k, bd + 2 * k, instr_desc(128, BT), k > 0);
+                for (int k = 0; k < 4; ++k) mma<1>(tmem + b * BT, a + 2 * k, bd + 2 * k, instr_desc(128, BT), k > 0);
                 mma_commit<1>(empty + s);
                 mma_commit<1>(tfull + b);
             }
+            __syncwarp();
         }
     } else {
         // the scale of x's row `tid` for the next block: loaded a block ahead, handed to the other
@@ -119,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
             asm volatile("bar.sync 1, 128;" ::: "memory");
             const int b = i % S::kBuffers;
             // after a wait that gave up the warps go on meeting at the barrier, without work
-            if (!__all_sync(0xffffffffu, mbar_wait(tfull + b, (i / S::kBuffers) & 1, failed, status))) continue;
+            if (!mbar_wait_warp(tfull + b, (i / S::kBuffers) & 1, failed, status)) continue;
             fence_after();
             const uint32_t addr = tmem + ((uint32_t)(32 * warp) << 16) + b * BT;
             constexpr int W = BT < 32 ? 16 : 32;

@@ -23,15 +23,17 @@ namespace {
 
 using namespace harp_tc;
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+constexpr int kSumRegs = 232, kOtherRegs = 40;   // registers per thread after the split: 2 x 232 + 40 = 3 x 168 at launch
 constexpr int kGroup = 16;   // tiles of rows that run together: their slices of x stay in L2 for every tile of the weight
 
 template <int NT>
 struct Shape {
     static constexpr int kA = 128 * 128, kB = NT / 2 * 128, kStageBytes = kA + kB;
     static constexpr int kStages = 6;
-    static constexpr int kBuffers = 2;
-    static constexpr int kCols = kBuffers * NT;
+    static constexpr int kHalf = NT / 2;       // columns of a product: half of the tile
+    static constexpr int kBuffers = 2;         // per half
+    static constexpr int kCols = 2 * kBuffers * kHalf;
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + 256;
 };
 
@@ -99,8 +101,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint64_t* full = reinterpret_cast<uint64_t*>(stages + S::kStages * S::kStageBytes);
     uint64_t* empty = full + S::kStages;
     uint64_t* tfull = empty + S::kStages;
-    uint64_t* tempty = tfull + S::kBuffers;
-    uint32_t* slot = reinterpret_cast<uint32_t*>(tempty + S::kBuffers);
+    uint64_t* tempty = tfull + 2 * S::kBuffers;   // both [half][buffer]
+    uint32_t* slot = reinterpret_cast<uint32_t*>(tempty + 2 * S::kBuffers);
     volatile int* failed = reinterpret_cast<volatile int*>(slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -113,7 +115,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tma_prefetch(&map_x);
         tma_prefetch(&map_w);
         for (int i = 0; i < S::kStages; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1);
-        for (int i = 0; i < S::kBuffers; ++i) mbar_init(tfull + i, 1), mbar_init(tempty + i, 16);
+        for (int i = 0; i < 2 * S::kBuffers; ++i) mbar_init(tfull + i, 1), mbar_init(tempty + i, 8);
         *failed = 0;
         mbar_init_fence();
     }
@@ -123,56 +125,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fence_after();
     const uint32_t tmem = *slot;
 
-    if (warp == 8) {
-        if (lane == 0) {
+    if (warp >= 8) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+      if (warp == 8) {
+        {
             int s = 0, ph = 0;
             int64_t used = 0;
             bool ok = true;
             for (int64_t t = pair; ok && t < tiles; t += pairs) {
                 const TileOf at = tile_of(t, mt, nt);
-                const int m0 = (int)(at.m * 256 + 128 * rank), n0 = (int)(at.n * NT + NT / 2 * rank);
+                const int m0 = (int)(at.m * 256 + 128 * rank), n0 = (int)(at.n * NT + NT / 4 * rank);
                 for (int k = 0; k < kb; ++k) {
-                    if (used >= S::kStages && !(ok = mbar_wait(empty + s, ph ^ 1, failed, status))) break;
+                    if (used >= S::kStages && !(ok = mbar_wait_warp(empty + s, ph ^ 1, failed, status))) break;
                     unsigned char* st = stages + s * S::kStageBytes;
                     const uint32_t bar = map_to_rank(smem_u32(full + s), 0);
+                    if (elect_one()) {
                     if (rank == 0) mbar_expect_tx(full + s, 2 * S::kStageBytes);
                     tma_load_pair(st, &map_x, k * 128, m0, bar);
                     tma_load_pair(st + S::kA, &map_w, k * 128, n0, bar);
+                    tma_load_pair(st + S::kA + S::kB / 2, &map_w, k * 128, n0 + S::kHalf, bar);
+                    }
+                    __syncwarp();
                     ++used;
                     if (++s == S::kStages) s = 0, ph ^= 1;
                 }
             }
             // the pair's last products have released every stage: no arrival on this CTA's barriers is left
             for (int i = 0; ok && i < S::kStages; ++i) {
-                if (used >= S::kStages) ok = mbar_wait(empty + s, ph ^ 1, failed, status);
-                else if (i < used) ok = mbar_wait(empty + i, 0, failed, status);
+                if (used >= S::kStages) ok = mbar_wait_warp(empty + s, ph ^ 1, failed, status);
+                else if (i < used) ok = mbar_wait_warp(empty + i, 0, failed, status);
                 if (++s == S::kStages) s = 0, ph ^= 1;
             }
         }
-    } else if (warp == 9) {
-        if (lane == 0 && rank == 0) {
+      } else if (warp == 9) {
+        if (rank == 0) {
             int s = 0, ph = 0, b = 0, bph = 0;
             int64_t used = 0;
             bool ok = true;
             for (int64_t t = pair; ok && t < tiles; t += pairs) {
                 for (int k = 0; k < kb; ++k) {
-                    if (!(ok = mbar_wait(full + s, ph, failed, status))) break;
-                    if (used >= S::kBuffers && !(ok = mbar_wait(tempty + b, bph ^ 1, failed, status))) break;
-                    fence_after();
+                    if (!(ok = mbar_wait_warp(full + s, ph, failed, status))) break;
                     const uint64_t a = operand_desc(stages + s * S::kStageBytes);
-                    const uint64_t w = operand_desc(stages + s * S::kStageBytes + S::kA);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mma<2>(tmem + b * NT, a + 2 * i, w + 2 * i, instr_desc(256, NT), i > 0);
-                    mma_commit<2>(empty + s);
-                    mma_commit<2>(tfull + b);
+                    for (int h = 0; ok && h < 2; ++h) {
+                        const int at = h * S::kBuffers + b;
+                        if (used >= S::kBuffers && !(ok = mbar_wait_warp(tempty + at, bph ^ 1, failed, status))) break;
+                        fence_after();
+                        const uint64_t w = operand_desc(stages + s * S::kStageBytes + S::kA + h * S::kB / 2);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                mma<2>(tmem + at * S::kHalf, a + 2 * i, w + 2 * i, instr_desc(256, S::kHalf), i > 0);
+                            if (h == 1) mma_commit<2>(empty + s);
+                            mma_commit<2>(tfull + at);
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
                     ++used;
                     if (++s == S::kStages) s = 0, ph ^= 1;
                     if (++b == S::kBuffers) b = 0, bph ^= 1;
                 }
             }
         }
+      }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
         constexpr int N = NT / 2;   // columns of this thread
         const int half = warp >> 2;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -193,27 +211,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int k = 0; k < kb; ++k) {
                 float x2 = 0.f, w2 = 0.f;
                 if (k + 2 < kb) x2 = row ? __ldg(sx + k + 2) : 0.f, w2 = __ldg(sw + k + 2);
-                ok = __all_sync(0xffffffffu, mbar_wait(tfull + b, bph, failed, status));
+                const int buf = half * S::kBuffers + b;
+                ok = mbar_wait_warp(tfull + buf, bph, failed, status);
                 if (!ok) break;
                 fence_after();
                 const float f = x0 * w0;
                 x0 = x1, w0 = w1, x1 = x2, w1 = w2;
-                const uint32_t addr = tmem + lanes + b * NT + N * half;
-                uint32_t v[2][16];
-                tmem_ld(addr, v[0]);
+                const uint32_t addr = tmem + lanes + buf * S::kHalf;
+                uint32_t u[32], v[32];
+                tmem_ld(addr, u);
+                tmem_ld(addr + 32, v);
+                tmem_ld_wait(u);
+                tmem_ld_wait(v);
 #pragma unroll
-                for (int i = 0; i < N / 16; ++i) {
-                    tmem_ld_wait(v[i & 1]);
-                    if (i + 1 < N / 16) {
-                        tmem_ld(addr + 16 * (i + 1), v[(i + 1) & 1]);
-                    } else {
-                        fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(tempty + b), 0));
-                    }
+                for (int c = 0; c < 32; c += 2) fma2(sum[c], sum[c + 1], u[c], u[c + 1], f);
+                if constexpr (N == 128) {
+                    tmem_ld(addr + 64, u);
 #pragma unroll
-                    for (int c = 0; c < 16; c += 2) fma2(sum[16 * i + c], sum[16 * i + c + 1], v[i & 1][c], v[i & 1][c + 1], f);
+                    for (int c = 0; c < 32; c += 2) fma2(sum[32 + c], sum[33 + c], v[c], v[c + 1], f);
+                    tmem_ld(addr + 96, v);
+                    tmem_ld_wait(u);
+                    tmem_ld_wait(v);
                 }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(tempty + buf), 0));
+                if constexpr (N == 128) {
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) fma2(sum[64 + c], sum[65 + c], u[c], u[c + 1], f);
+                }
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) fma2(sum[N - 32 + c], sum[N - 31 + c], v[c], v[c + 1], f);
                 if (++b == S::kBuffers) b = 0, bph ^= 1;
             }
             if (ok && row && c0 < p.n) store_row<N>((T*)p.y + r * p.ld_y + c0, p.n - c0, vec, sum);
@@ -235,7 +263,7 @@ harp_status launch(const MatmulParams& p, cudaStream_t stream) {
     CUtensorMap mx, mw;
     harp_status st;
     if ((st = matmul_tensor_map(&mx, p.x, p.rows, p.k, p.ld_x, 128)) != HARP_OK) return st;
-    if ((st = matmul_tensor_map(&mw, p.w, p.n, p.k, p.ld_w, NT / 2)) != HARP_OK) return st;
+    if ((st = matmul_tensor_map(&mw, p.w, p.n, p.k, p.ld_w, NT / 4)) != HARP_OK) return st;
     int* status = matmul_status_word();
     if (!status) return harp_fail(HARP_ERR_CUDA, "the device's status word has no address");
     const size_t es = sizeof(T);

@@ -8,7 +8,7 @@
 
 namespace harp_tc {
 
-constexpr int kWaitLimit = 1 << 24;   // mbarrier polls before a wait gives up
+constexpr long long kWaitClocks = 4000000000ll;   // about two seconds: then a wait gives up
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -24,6 +24,15 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// One lane of a converged warp.  The tcgen05 and TMA instructions take their operands from uniform
+// registers: issued under this predicate from a loop that the whole warp runs they cost a few
+// cycles, from a loop of one lane about a hundred each.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
 }
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
@@ -47,7 +56,8 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
 // shared memory, which ends the CTA's other waits too) and the device's status word.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* failed, int* status) {
     const uint32_t addr = smem_u32(bar);
-    for (int i = 0; i < kWaitLimit; ++i) {
+    long long t0 = 0;
+    for (int i = 0;; ++i) {
         uint32_t done;
         asm volatile(
             "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; "
@@ -56,11 +66,21 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
             : "r"(addr), "r"(parity)
             : "memory");
         if (done) return true;
-        if ((i & 63) == 63 && *failed) return false;
+        if ((i & 63) == 63) {
+            if (*failed) return false;
+            if (i == 63) t0 = clock64();
+            else if (clock64() - t0 > kWaitClocks) break;
+        }
+        if (i == 1 << 30) break;
     }
     *failed = 1;
     atomicExch(status, 1);
     return false;
+}
+
+// The same for a converged warp, with one answer for all lanes.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* failed, int* status) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, failed, status));
 }
 
 // After a wait that gave up: time for the copies in flight to land (they end by themselves).
