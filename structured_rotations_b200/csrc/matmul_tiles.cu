@@ -2,14 +2,23 @@
 //
 // Per block of 128 along k the pair multiplies 256 rows of x by NT rows of the weight with
 // tcgen05.mma.cta_group::2 (each CTA holds its own 128 rows of x and half of the weight's tile, so
-// every byte that it loads is used by both): 64 bytes of operands per SM and clock at the full
-// e4m3 rate, against 96 for a CTA alone on 128 x 256.  The scales differ from block to
-// block, so a block's sums cannot stay in tensor memory: they go into one of two buffers of NT
-// columns, and while the tensor cores work on the next block, eight warps read the finished
-// buffer, scale it and add it to fp32 sums in registers (128 per thread at NT = 256).
+// every byte that it loads is used by both): at NT = 256, 64 bytes of operands per SM and clock at
+// the full e4m3 rate, against 96 for a CTA alone on 128 x 256.  The scales differ from block to
+// block, so a block's sums cannot stay in tensor memory: they go into one of 512 / NT buffers, and
+// while the tensor cores work on the next blocks, eight warps read the finished buffer, scale it and
+// add it to fp32 sums in registers (128 per thread at NT = 256).
 //   warps 0-7  sums: thread = one row of x (a lane of tensor memory) and NT / 2 columns
 //   warp 8     TMA loads of this CTA's operands, completing on the leader's barrier
 //   warp 9     tensor-memory allocation; in the leader (rank 0) tcgen05.mma for both CTAs
+//
+// What bounds it: a buffer is held for its products (512 clocks at NT = 256, the full rate), 270
+// clocks until the waiting warps see them done, 400-450 for taking it into registers (half of the
+// additions among the loads: registers do not hold a whole buffer beside the sums), and up to 370
+// until the leader sees the other CTA's arrivals; with both of tensor memory's halves
+// held that long a block takes about 900 clocks.  Measured on 4096 x 28672 x 8192: 0.87 ms (2.2
+// PFLOP/s); 0.68 ms without reading the buffers, 0.73 ms reading but not adding them.  Tried and
+// no faster: halves of 128 columns with their own buffers, 192 columns with all loads before
+// the additions, scales by another warp, results by TMA stores.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -23,18 +32,17 @@ namespace {
 
 using namespace harp_tc;
 
-constexpr int kThreads = 384;
-constexpr int kSumRegs = 232, kOtherRegs = 40;   // registers per thread after the split: 2 x 232 + 40 = 3 x 168 at launch
+constexpr int kThreads = 320;
 constexpr int kGroup = 16;   // tiles of rows that run together: their slices of x stay in L2 for every tile of the weight
 
 template <int NT>
 struct Shape {
     static constexpr int kA = 128 * 128, kB = NT / 2 * 128, kStageBytes = kA + kB;
-    static constexpr int kStages = 6;
-    static constexpr int kHalf = NT / 2;       // columns of a product: half of the tile
-    static constexpr int kBuffers = 2;         // per half
-    static constexpr int kCols = 2 * kBuffers * kHalf;
-    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + 256;
+    static constexpr int kStages = NT == 256 ? 6 : 8;
+    static constexpr int kBuffers = 512 / NT;
+    static constexpr int kCols = kBuffers * NT;
+    static constexpr int kOutFloats = 32 * 17;   // per warp: 32 rows x 16 results, padded
+    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + 8 * kOutFloats * 4 + 256;
 };
 
 struct TileOf {
@@ -51,58 +59,54 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&p);
 }
-__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
-                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// Row of N sums (c0 columns of n left): 32-byte stores where `vec`.
-template <int N>
-__device__ __forceinline__ void store_row(float* y, int64_t left, bool vec, const float (&v)[N]) {
-    if (vec && left >= N) {
-#pragma unroll
-        for (int c = 0; c < N; c += 8) {
-            uint32_t w[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(v[c + k]);
-            store32(y + c, w);
-        }
+// 32 bytes of results, as one store where `wide` (32-byte aligned), else as two.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
     } else {
-#pragma unroll
-        for (int c = 0; c < N; ++c)
-            if (c < left) y[c] = v[c];
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
     }
 }
 template <int N>
-__device__ __forceinline__ void store_row(__nv_bfloat16* y, int64_t left, bool vec, const float (&v)[N]) {
-    if (vec && left >= N) {
+__device__ __forceinline__ void store_row(float* y, const float (&v)[N], bool wide) {
 #pragma unroll
-        for (int c = 0; c < N; c += 16) {
-            uint32_t w[8];
+    for (int c = 0; c < N; c += 8) {
+        uint32_t w[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = pack2(v[c + 2 * k], v[c + 2 * k + 1]);
-            store32(y + c, w);
-        }
-    } else {
+        for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(v[c + k]);
+        store32(y + c, w, wide);
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_row(__nv_bfloat16* y, const float (&v)[N], bool wide) {
 #pragma unroll
-        for (int c = 0; c < N; ++c)
-            if (c < left) y[c] = __float2bfloat16_rn(v[c]);
+    for (int c = 0; c < N; c += 16) {
+        uint32_t w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = pack2(v[c + 2 * k], v[c + 2 * k + 1]);
+        store32(y + c, w, wide);
     }
 }
 
 template <int NT, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     matmul_tiles_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-                        const __grid_constant__ MatmulParams p, int64_t mt, int64_t nt, bool vec, int* status) {
+                        const __grid_constant__ MatmulParams p, int64_t mt, int64_t nt, int align_y, int* status) {
     using S = Shape<NT>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* stages = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint64_t* full = reinterpret_cast<uint64_t*>(stages + S::kStages * S::kStageBytes);
+    float* out = reinterpret_cast<float*>(stages + S::kStages * S::kStageBytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(out + 8 * S::kOutFloats);
     uint64_t* empty = full + S::kStages;
     uint64_t* tfull = empty + S::kStages;
-    uint64_t* tempty = tfull + 2 * S::kBuffers;   // both [half][buffer]
-    uint32_t* slot = reinterpret_cast<uint32_t*>(tempty + 2 * S::kBuffers);
+    uint64_t* tempty = tfull + S::kBuffers;
+    uint32_t* slot = reinterpret_cast<uint32_t*>(tempty + S::kBuffers);
     volatile int* failed = reinterpret_cast<volatile int*>(slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -115,7 +119,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tma_prefetch(&map_x);
         tma_prefetch(&map_w);
         for (int i = 0; i < S::kStages; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1);
-        for (int i = 0; i < 2 * S::kBuffers; ++i) mbar_init(tfull + i, 1), mbar_init(tempty + i, 8);
+        for (int i = 0; i < S::kBuffers; ++i) mbar_init(tfull + i, 1), mbar_init(tempty + i, 16);
         *failed = 0;
         mbar_init_fence();
     }
@@ -125,75 +129,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fence_after();
     const uint32_t tmem = *slot;
 
-    if (warp >= 8) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-      if (warp == 8) {
-        {
-            int s = 0, ph = 0;
-            int64_t used = 0;
-            bool ok = true;
-            for (int64_t t = pair; ok && t < tiles; t += pairs) {
-                const TileOf at = tile_of(t, mt, nt);
-                const int m0 = (int)(at.m * 256 + 128 * rank), n0 = (int)(at.n * NT + NT / 4 * rank);
-                for (int k = 0; k < kb; ++k) {
-                    if (used >= S::kStages && !(ok = mbar_wait_warp(empty + s, ph ^ 1, failed, status))) break;
+    if (warp == 8) {
+        int s = 0, ph = 0;
+        int64_t used = 0;
+        bool ok = true;
+        for (int64_t t = pair; ok && t < tiles; t += pairs) {
+            const TileOf at = tile_of(t, mt, nt);
+            const int m0 = (int)(at.m * 256 + 128 * rank), n0 = (int)(at.n * NT + NT / 2 * rank);
+            for (int k = 0; k < kb; ++k) {
+                if (used >= S::kStages && !(ok = mbar_wait_warp(empty + s, ph ^ 1, failed, status))) break;
+                if (elect_one()) {
                     unsigned char* st = stages + s * S::kStageBytes;
                     const uint32_t bar = map_to_rank(smem_u32(full + s), 0);
-                    if (elect_one()) {
                     if (rank == 0) mbar_expect_tx(full + s, 2 * S::kStageBytes);
                     tma_load_pair(st, &map_x, k * 128, m0, bar);
                     tma_load_pair(st + S::kA, &map_w, k * 128, n0, bar);
-                    tma_load_pair(st + S::kA + S::kB / 2, &map_w, k * 128, n0 + S::kHalf, bar);
-                    }
-                    __syncwarp();
-                    ++used;
-                    if (++s == S::kStages) s = 0, ph ^= 1;
                 }
-            }
-            // the pair's last products have released every stage: no arrival on this CTA's barriers is left
-            for (int i = 0; ok && i < S::kStages; ++i) {
-                if (used >= S::kStages) ok = mbar_wait_warp(empty + s, ph ^ 1, failed, status);
-                else if (i < used) ok = mbar_wait_warp(empty + i, 0, failed, status);
+                __syncwarp();
+                ++used;
                 if (++s == S::kStages) s = 0, ph ^= 1;
             }
         }
-      } else if (warp == 9) {
-        if (rank == 0) {
-            int s = 0, ph = 0, b = 0, bph = 0;
-            int64_t used = 0;
-            bool ok = true;
-            for (int64_t t = pair; ok && t < tiles; t += pairs) {
-                for (int k = 0; k < kb; ++k) {
-                    if (!(ok = mbar_wait_warp(full + s, ph, failed, status))) break;
+        // the pair's last products have released every stage: no arrival on this CTA's barriers is left
+        for (int i = 0; ok && i < S::kStages; ++i) {
+            if (used >= S::kStages) ok = mbar_wait_warp(empty + s, ph ^ 1, failed, status);
+            else if (i < used) ok = mbar_wait_warp(empty + i, 0, failed, status);
+            if (++s == S::kStages) s = 0, ph ^= 1;
+        }
+    } else if (warp == 9) {
+        int s = 0, ph = 0, b = 0, bph = 0;
+        int64_t used = 0;
+        bool ok = true, ready = false;   // ready: the next stage was seen full while the last products were issued
+        for (int64_t t = pair; ok && rank == 0 && t < tiles; t += pairs) {
+            for (int k = 0; k < kb; ++k) {
+                if (!ready && !(ok = mbar_wait_warp(full + s, ph, failed, status))) break;
+                if (used >= S::kBuffers && !(ok = mbar_wait_warp(tempty + b, bph ^ 1, failed, status))) break;
+                fence_after();
+                if (elect_one()) {
                     const uint64_t a = operand_desc(stages + s * S::kStageBytes);
+                    const uint64_t w = operand_desc(stages + s * S::kStageBytes + S::kA);
 #pragma unroll
-                    for (int h = 0; ok && h < 2; ++h) {
-                        const int at = h * S::kBuffers + b;
-                        if (used >= S::kBuffers && !(ok = mbar_wait_warp(tempty + at, bph ^ 1, failed, status))) break;
-                        fence_after();
-                        const uint64_t w = operand_desc(stages + s * S::kStageBytes + S::kA + h * S::kB / 2);
-                        if (elect_one()) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                mma<2>(tmem + at * S::kHalf, a + 2 * i, w + 2 * i, instr_desc(256, S::kHalf), i > 0);
-                            if (h == 1) mma_commit<2>(empty + s);
-                            mma_commit<2>(tfull + at);
-                        }
-                        __syncwarp();
-                    }
-                    if (!ok) break;
-                    ++used;
-                    if (++s == S::kStages) s = 0, ph ^= 1;
-                    if (++b == S::kBuffers) b = 0, bph ^= 1;
+                    for (int i = 0; i < 4; ++i) mma<2>(tmem + b * NT, a + 2 * i, w + 2 * i, instr_desc(256, NT), i > 0);
+                    mma_commit<2>(tfull + b);
+                    mma_commit<2>(empty + s);
                 }
+                __syncwarp();
+                ++used;
+                if (++s == S::kStages) s = 0, ph ^= 1;
+                if (++b == S::kBuffers) b = 0, bph ^= 1;
+                ready = mbar_test_warp(full + s, ph);
             }
         }
-      }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
         constexpr int N = NT / 2;   // columns of this thread
         const int half = warp >> 2;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        float* mine = out + warp * S::kOutFloats;
+        const uint32_t back = map_to_rank(smem_u32(tempty), 0);
         int b = 0, bph = 0;
         bool ok = true;
         for (int64_t t = pair; ok && t < tiles; t += pairs) {
@@ -211,40 +203,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int k = 0; k < kb; ++k) {
                 float x2 = 0.f, w2 = 0.f;
                 if (k + 2 < kb) x2 = row ? __ldg(sx + k + 2) : 0.f, w2 = __ldg(sw + k + 2);
-                const int buf = half * S::kBuffers + b;
-                ok = mbar_wait_warp(tfull + buf, bph, failed, status);
+                ok = mbar_wait_warp(tfull + b, bph, failed, status);
                 if (!ok) break;
                 fence_after();
                 const float f = x0 * w0;
                 x0 = x1, w0 = w1, x1 = x2, w1 = w2;
-                const uint32_t addr = tmem + lanes + buf * S::kHalf;
-                uint32_t u[32], v[32];
-                tmem_ld(addr, u);
-                tmem_ld(addr + 32, v);
-                tmem_ld_wait(u);
-                tmem_ld_wait(v);
+                const uint32_t addr = tmem + lanes + b * NT + N * half;
+                uint32_t v[2][16];
+                tmem_ld(addr, v[0]);
 #pragma unroll
-                for (int c = 0; c < 32; c += 2) fma2(sum[c], sum[c + 1], u[c], u[c + 1], f);
-                if constexpr (N == 128) {
-                    tmem_ld(addr + 64, u);
+                for (int i = 0; i < N / 16; ++i) {
+                    tmem_ld_wait(v[i & 1]);
+                    if (i + 1 < N / 16) {
+                        tmem_ld(addr + 16 * (i + 1), v[(i + 1) & 1]);
+                    } else {
+                        fence_before();
+                        __syncwarp();
+                        if (elect_one()) mbar_arrive_cluster(back + 8 * b);
+                    }
 #pragma unroll
-                    for (int c = 0; c < 32; c += 2) fma2(sum[32 + c], sum[33 + c], v[c], v[c + 1], f);
-                    tmem_ld(addr + 96, v);
-                    tmem_ld_wait(u);
-                    tmem_ld_wait(v);
+                    for (int c = 0; c < 16; c += 2) fma2(sum[16 * i + c], sum[16 * i + c + 1], v[i & 1][c], v[i & 1][c + 1], f);
                 }
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(tempty + buf), 0));
-                if constexpr (N == 128) {
-#pragma unroll
-                    for (int c = 0; c < 32; c += 2) fma2(sum[64 + c], sum[65 + c], u[c], u[c + 1], f);
-                }
-#pragma unroll
-                for (int c = 0; c < 32; c += 2) fma2(sum[N - 32 + c], sum[N - 31 + c], v[c], v[c + 1], f);
                 if (++b == S::kBuffers) b = 0, bph ^= 1;
             }
-            if (ok && row && c0 < p.n) store_row<N>((T*)p.y + r * p.ld_y + c0, p.n - c0, vec, sum);
+            if (!ok) break;
+            if (c0 >= p.n) continue;
+            if (align_y >= 16 && c0 + N <= p.n) {
+                if (row) store_row((T*)p.y + r * p.ld_y + c0, sum, align_y >= 32);
+                continue;
+            }
+            // 16 columns at a time through shared memory: two rows of 16 consecutive results per store
+            const int64_t r0 = r - lane;
+#pragma unroll
+            for (int i = 0; i < N / 16; ++i) {
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 16; ++c) mine[lane * 17 + c] = sum[16 * i + c];
+                __syncwarp();
+                const int64_t c = c0 + 16 * i + (lane & 15);
+                if (c < p.n) {
+#pragma unroll 8
+                    for (int j = lane >> 4; j < 32; j += 2)
+                        if (r0 + j < p.rows) put((T*)p.y + (r0 + j) * p.ld_y + c, mine[j * 17 + (lane & 15)]);
+                }
+            }
         }
     }
     __syncwarp();
@@ -263,16 +265,16 @@ harp_status launch(const MatmulParams& p, cudaStream_t stream) {
     CUtensorMap mx, mw;
     harp_status st;
     if ((st = matmul_tensor_map(&mx, p.x, p.rows, p.k, p.ld_x, 128)) != HARP_OK) return st;
-    if ((st = matmul_tensor_map(&mw, p.w, p.n, p.k, p.ld_w, NT / 4)) != HARP_OK) return st;
+    if ((st = matmul_tensor_map(&mw, p.w, p.n, p.k, p.ld_w, NT / 2)) != HARP_OK) return st;
     int* status = matmul_status_word();
     if (!status) return harp_fail(HARP_ERR_CUDA, "the device's status word has no address");
-    const size_t es = sizeof(T);
-    const bool vec = (uintptr_t)p.y % 32 == 0 && ((size_t)p.ld_y * es) % 32 == 0;
+    const uint64_t to = (uint64_t)(uintptr_t)p.y | (uint64_t)p.ld_y * sizeof(T);
+    const int align_y = to % 32 == 0 ? 32 : to % 16 == 0 ? 16 : 1;
     auto kern = matmul_tiles_kernel<NT, T>;
     cudaError_t e = (cudaError_t)harp_set_smem_limit((const void*)kern, (int)S::kSmem);
     if (e == cudaSuccess) {
         const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(mt * nt, harp_sm_count() / 2));
-        kern<<<(unsigned)(2 * pairs), kThreads, S::kSmem, stream>>>(mx, mw, p, mt, nt, vec, status);
+        kern<<<(unsigned)(2 * pairs), kThreads, S::kSmem, stream>>>(mx, mw, p, mt, nt, align_y, status);
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) {
@@ -287,5 +289,11 @@ harp_status launch(const MatmulParams& p, cudaStream_t stream) {
 
 harp_status launch_matmul_tiles(const MatmulParams& p, harp_dtype out, void* stream) {
     cudaStream_t s = (cudaStream_t)stream;
+    // The narrower tile where it leaves fewer pairs idle: a block of 256 x 128 takes about 0.6 of the time of
+    // one of 256 x 256, so with t tiles of 256 columns on P pairs it wins when ceil(2 t / P) 0.6 < ceil(t / P).
+    const int64_t pairs = std::max(1, harp_sm_count() / 2), mt = (p.rows + 255) / 256;
+    const int64_t wide = (mt * ((p.n + 255) / 256) + pairs - 1) / pairs, narrow = (mt * ((p.n + 127) / 128) + pairs - 1) / pairs;
+    if (3 * narrow < 5 * wide)
+        return out == HARP_F32 ? launch<128, float>(p, s) : launch<128, __nv_bfloat16>(p, s);
     return out == HARP_F32 ? launch<256, float>(p, s) : launch<256, __nv_bfloat16>(p, s);
 }

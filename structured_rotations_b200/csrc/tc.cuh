@@ -83,6 +83,17 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, v
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, failed, status));
 }
 
+// Whether the phase is over now (false says nothing), the same answer for all lanes of a converged warp.
+__device__ __forceinline__ bool mbar_test_warp(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return __all_sync(0xffffffffu, done);
+}
+
 // After a wait that gave up: time for the copies in flight to land (they end by themselves).
 __device__ __forceinline__ void drain_delay() {
     const long long t0 = clock64();
@@ -106,6 +117,20 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map,
 }
 __device__ __forceinline__ void tma_prefetch(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// A 4-byte copy from global to shared memory that no register waits for; copies retire in groups.
+__device__ __forceinline__ void copy4_async(const void* dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// The first `bytes` of 16, zeros behind them; both addresses 16-byte aligned.
+__device__ __forceinline__ void copy16_async(const void* dst, const float* src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {   // all but the last N groups have landed
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Tensor memory.  G: CTAs that share an instruction (1, or 2 for a CTA pair).
