@@ -1,7 +1,7 @@
 // Root-mean-square norm with the residual's addition and an 8-bit output (the layer's entry in
 // front of a blockwise quantizer, HARP technical summary §2.4; codes and scales in codes.cuh):
 //   h = rn_T(rn32(x + residual))              (h = x without a residual)
-//   r = rn32(1 / sqrt(sum_j h_j^2 / d + eps)) (the sum, the quotient and the root in double)
+//   r = rn32(1 / sqrt(sum_j h_j^2 / d + eps)) (the sum, its mean and the root in double)
 //   u = rn32(rn32(h r) w)                     (w = 1 without a weight)
 // and u's codes and scales, u itself rounded to T, or both.  One pass: a row stays in the
 // registers of the threads that share it, between the sum and the codes.  The sum is taken
@@ -24,7 +24,7 @@ struct NormParams {
     const void *x, *res, *w;
     int64_t rows, ld_x, ld_r;
     int d;
-    double eps;
+    double eps, inv_d;
     void *h, *y;
     int64_t ld_h, ld_y;
     uint8_t* q;
@@ -35,50 +35,42 @@ struct NormParams {
     bool vx, vr, vw, vh, vy, vq;   // vector access of each array
 };
 
-template <typename T>
-__device__ __forceinline__ float round_to(float v);
-template <>
-__device__ __forceinline__ float round_to<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ float round_to<__nv_bfloat16>(float v) { return __bfloat162float(__float2bfloat16_rn(v)); }
-
-// blockDim.x threads share a row (a multiple of 32), blockDim.y rows per CTA; a thread holds N
+// blockDim.x threads share a row (a multiple of 32), blockDim.y rows per CTA of at most MOST threads; a thread holds N
 // groups of 8 coordinates, group i at 8 (i blockDim.x + threadIdx.x).
-template <typename T, typename C, int N>
-__global__ void __launch_bounds__(1024) rms_norm_quant_kernel(const __grid_constant__ NormParams p) {
+template <typename T, typename C, int N, int MOST>
+__global__ void __launch_bounds__(MOST) rms_norm_quant_kernel(const __grid_constant__ NormParams p) {
     __shared__ double part[32];
     const int tx = threadIdx.x, nx = blockDim.x;
     const int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const bool live = r < p.rows;
-    float v[N][8];
+    const int64_t c0 = 8 * (tx & ~31), step = 8 * nx;
+    Eight<T> h8[N];   // the row's sum, in T
     double sum = 0.0;
+    if (live) {
+        load_groups<T, N>((const T*)p.x + r * p.ld_x, c0, step, p.d, p.vx, h8);
+        if (p.res) {
+            Eight<T> e8[N];
+            load_groups<T, N>((const T*)p.res + r * p.ld_r, c0, step, p.d, p.vr, e8);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int c = 8 * (i * nx + tx), n = live ? min(8, p.d - c) : 0;
+            for (int i = 0; i < N; ++i) {
+                float v[8], e[8];
+                h8[i].get(v);
+                e8[i].get(e);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
-        if (n > 0) load8((const T*)p.x + r * p.ld_x + c, n, p.vx, v[i]);
-    }
-    if (p.res) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int c = 8 * (i * nx + tx), n = live ? min(8, p.d - c) : 0;
-            if (n > 0) {
-                float e[8];
-                load8((const T*)p.res + r * p.ld_r + c, n, p.vr, e);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[i][k] = round_to<T>(v[i][k] + e[k]);
+                for (int k = 0; k < 8; ++k) v[k] += e[k];
+                h8[i].set(v);
             }
         }
-    }
+        if (p.h) store_groups<T, N>((T*)p.h + r * p.ld_h, c0, step, p.d, p.vh, h8);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int c = 8 * (i * nx + tx), n = live ? min(8, p.d - c) : 0;
-        if (p.h && n > 0) store8((T*)p.h + r * p.ld_h + c, n, p.vh, v[i]);
+        for (int i = 0; i < N; ++i) {
+            float v[8];
+            h8[i].get(v);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const double t = (double)v[i][k];
-            sum = fma(t, t, sum);
+            for (int k = 0; k < 8; ++k) {
+                const double t = (double)v[k];
+                sum = fma(t, t, sum);
+            }
         }
     }
 #pragma unroll
@@ -90,42 +82,48 @@ __global__ void __launch_bounds__(1024) rms_norm_quant_kernel(const __grid_const
         sum = 0.0;
         for (int w = 0; w < wpr; ++w) sum += part[w0 + w];
     }
-    const float rs = (float)(1.0 / sqrt(sum / (double)p.d + p.eps));
-    const int qlanes = p.qblock / 8;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int c = 8 * (i * nx + tx), n = live ? min(8, p.d - c) : 0;
-        float a = 0.f;
+    const float rs = (float)rsqrt(sum * p.inv_d + p.eps);
+    if (!live) return;
+    // group i of u
+    const bool whole = whole_groups<N>(c0, step, p.d);
+    auto u = [&](int i, float(&v)[8]) {
+        h8[i].get(v);
+        const int c = 8 * (i * nx + tx);
         if (p.w) {
             float g[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (n > 0) load8((const T*)p.w + c, n, p.vw, g);
+            if (whole || c < p.d) load8_cached((const T*)p.w + c, whole ? 8 : min(8, p.d - c), p.vw, g);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[i][k] = __fmul_rn(__fmul_rn(v[i][k], rs), g[k]);
+            for (int k = 0; k < 8; ++k) v[k] = __fmul_rn(__fmul_rn(v[k], rs), g[k]);
         } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[i][k] = __fmul_rn(v[i][k], rs);
+            for (int k = 0; k < 8; ++k) v[k] = __fmul_rn(v[k], rs);
         }
-        if (p.y && n > 0) store8((T*)p.y + r * p.ld_y + c, n, p.vy, v[i]);
-        if (p.q) {
+        if (!whole) {   // nothing there takes part in the row's last block, a NaN row's zeros neither
 #pragma unroll
-            for (int k = 0; k < 8; ++k) a = amax_nan(a, k < n ? v[i][k] : 0.f);
-            for (int o = 1; o < qlanes; o <<= 1) a = amax_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
-            if (n > 0) {
-                store_codes8<C>(p.q + r * p.ld_q + c, n, p.vq, v[i], code_factor<C>(a));
-                if ((tx & (qlanes - 1)) == 0) p.s[r * p.ld_s + c / p.qblock] = code_scale<C>(a);
-            }
+            for (int k = 0; k < 8; ++k)
+                if (c + k >= p.d) v[k] = 0.f;
         }
+    };
+    if (p.y) {
+        Eight<T> y8[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float v[8];
+            u(i, v);
+            y8[i].set(v);
+        }
+        store_groups<T, N>((T*)p.y + r * p.ld_y, c0, step, p.d, p.vy, y8);
     }
+    if (p.q) quantize_groups<C, N>(u, c0, step, p.d, p.qblock / 8, p.q + r * p.ld_q, p.vq, p.s + r * p.ld_s);
 }
 
 template <typename T, typename C>
 cudaError_t launch(const NormParams& p, int n, dim3 block, cudaStream_t stream) {
     const unsigned grid = (unsigned)((p.rows + block.y - 1) / block.y);
-    switch (n) {
-        case 1: rms_norm_quant_kernel<T, C, 1><<<grid, block, 0, stream>>>(p); break;
-        case 2: rms_norm_quant_kernel<T, C, 2><<<grid, block, 0, stream>>>(p); break;
-        default: rms_norm_quant_kernel<T, C, 4><<<grid, block, 0, stream>>>(p); break;
-    }
+    if (n == 1) rms_norm_quant_kernel<T, C, 1, 1024><<<grid, block, 0, stream>>>(p);
+    else if (n == 2) rms_norm_quant_kernel<T, C, 2, 256><<<grid, block, 0, stream>>>(p);
+    else if (block.x * block.y <= 256) rms_norm_quant_kernel<T, C, 4, 256><<<grid, block, 0, stream>>>(p);
+    else rms_norm_quant_kernel<T, C, 4, 1024><<<grid, block, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -186,19 +184,17 @@ extern "C" harp_status harp_rms_norm_quant(const void* x, int64_t ld_x, const vo
     p.x = x, p.res = residual, p.w = weight;
     p.rows = rows, p.ld_x = ld_x, p.ld_r = ld_r;
     p.d = (int)d;
-    p.eps = eps;
+    p.eps = eps, p.inv_d = 1.0 / (double)d;
     p.h = h, p.y = y, p.ld_h = ld_h, p.ld_y = ld_y;
     p.q = (uint8_t*)q, p.ld_q = ld_q, p.s = scales, p.ld_s = ld_s;
     p.qblock = qblock;
     p.vx = aligned(x, ld_x, es, 16), p.vr = aligned(residual, ld_r, es, 16), p.vw = aligned(weight, 0, es, 16);
     p.vh = aligned(h, ld_h, es, 16), p.vy = aligned(y, ld_y, es, 16), p.vq = aligned(q, ld_q, 1, 8);
-    // threads per row: as many as give each at most 4 groups of 8 coordinates; several short rows
-    // share a CTA of 256 threads
+    // Four groups of 8 coordinates per thread, which keeps enough loads of enough rows under way; one where
+    // the rows leave SMs idle; several short rows to a CTA of 256 threads.
     const int groups = (int)((d + 7) / 8);
-    int nx = 32, n = 1;
-    while (nx < 256 && nx < groups) nx *= 2;
-    while (n < 4 && nx * n < groups) n *= 2;
-    while (nx * n < groups) nx *= 2;
+    const int n = rows <= harp_sm_count() && groups <= 1024 ? 1 : groups <= 64 ? 2 : 4;
+    const int nx = (groups + 32 * n - 1) / (32 * n) * 32;
     const dim3 block((unsigned)nx, (unsigned)std::max(1, 256 / nx));
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;

@@ -26,31 +26,33 @@ struct QuantParams {
     int64_t ld_q;
     float* s;
     int64_t ld_s;
-    int qblock;      // coordinates per block along a row
+    int qblock, qshift;   // coordinates per block along a row, and their log2
     bool vx, vq;     // 16-byte loads of x, 8-byte stores of codes
 };
 
-// Blocks of 1 x q: a warp takes 256 consecutive coordinates of a row, 8 per lane, so a block is
-// the q / 8 lanes that share it and its maximum a few shuffles.
-template <typename T, typename C>
+// A warp's unit of work: N groups of 256 consecutive coordinates of a row.
+struct Unit {
+    int64_t r, c0;
+};
+template <int N>
+__device__ __forceinline__ Unit unit_of(int64_t u, int64_t units, int64_t per_row) {
+    int64_t r;
+    if (units <= 0x7fffffff) r = (uint32_t)u / (uint32_t)per_row;
+    else r = u / per_row;
+    return {r, (u - r * per_row) * 256 * N};
+}
+
+// Blocks of 1 x q: 8 coordinates per lane, so a block is q / 8 lanes of a group.
+template <typename T, typename C, int N>
 __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantParams p) {
-    const int lane = threadIdx.x & 31;
-    const int64_t chunks = (p.cols + 255) / 256, units = p.rows * chunks;
+    const int64_t per_row = (p.cols + 256 * N - 1) / (256 * N), units = p.rows * per_row;
     const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-    const int qlanes = p.qblock / 8;
     for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < units; u += warps) {
-        const int64_t r = u / chunks, c = (u - r * chunks) * 256 + 8 * lane;
-        const int n = (int)max((int64_t)0, min((int64_t)8, p.cols - c));
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (n > 0) load8((const T*)p.x + r * p.ld_x + c, n, p.vx, v);
-        float a = 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) a = amax_nan(a, v[k]);
-        for (int o = 1; o < qlanes; o <<= 1) a = amax_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
-        if (n > 0) {
-            store_codes8<C>(p.q + r * p.ld_q + c, n, p.vq, v, code_factor<C>(a));
-            if ((lane & (qlanes - 1)) == 0) p.s[r * p.ld_s + c / p.qblock] = code_scale<C>(a);
-        }
+        const Unit at = unit_of<N>(u, units, per_row);
+        const T* x = (const T*)p.x + at.r * p.ld_x;
+        Eight<T> x8[N];
+        load_groups<T, N>(x, at.c0, 256, p.cols, p.vx, x8);
+        quantize_groups<C, N>([&](int i, float(&v)[8]) { x8[i].get(v); }, at.c0, 256, p.cols, p.qblock / 8, p.q + at.r * p.ld_q, p.vq, p.s + at.r * p.ld_s);
     }
 }
 
@@ -62,19 +64,27 @@ __global__ void __launch_bounds__(kThreads) quantize_tiles_kernel(const QuantPar
     const int64_t tr = (int64_t)blockIdx.x / tc, tj = (int64_t)blockIdx.x % tc;
     const int64_t c = tj * 128 + 8 * (threadIdx.x & 15), r0 = tr * 128 + (threadIdx.x >> 4);
     const int n = (int)max((int64_t)0, min((int64_t)8, p.cols - c));
+    const bool whole = tj * 128 + 128 <= p.cols && tr * 128 + 128 <= p.rows;   // one path without conditions
     float v[8][8];
+    if (whole && p.vx) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            Eight<T> x;
+            x.load((const T*)p.x + (r0 + 16 * i) * p.ld_x + c);
+            x.get(v[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
+            const int64_t r = r0 + 16 * i;
+            if (n > 0 && r < p.rows) load8((const T*)p.x + r * p.ld_x + c, n, p.vx, v[i]);
+        }
+    }
     float a = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
-        const int64_t r = r0 + 16 * i;
-        if (n > 0 && r < p.rows) load8((const T*)p.x + r * p.ld_x + c, n, p.vx, v[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) a = amax_nan(a, v[i][k]);
+    for (int i = 0; i < 8; ++i) a = amax_nan(a, amax8(v[i]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a = amax_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = a;
@@ -82,38 +92,63 @@ __global__ void __launch_bounds__(kThreads) quantize_tiles_kernel(const QuantPar
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) a = amax_nan(a, part[w]);
     const float f = code_factor<C>(a);
+    if (whole && p.vq) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int64_t r = r0 + 16 * i;
-        if (n > 0 && r < p.rows) store_codes8<C>(p.q + r * p.ld_q + c, n, p.vq, v[i], f);
+        for (int i = 0; i < 8; ++i) store_codes8<C>(p.q + (r0 + 16 * i) * p.ld_q + c, 8, true, v[i], f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t r = r0 + 16 * i;
+            if (n > 0 && r < p.rows) store_codes8<C>(p.q + r * p.ld_q + c, n, p.vq, v[i], f);
+        }
     }
     if (threadIdx.x == 0) p.s[tr * p.ld_s + tj] = code_scale<C>(a);
 }
 
-// y = rn(code * scale), 8 coordinates per thread (they share a block).
-template <typename T, typename C>
+// y = rn(code * scale), 8 coordinates per lane (they share a block).
+template <typename T, typename C, int N>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const QuantParams p, T* y, int brows) {
-    const int64_t oct = (p.cols + 7) / 8, units = p.rows * oct;
-    for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < units; u += (int64_t)gridDim.x * kThreads) {
-        const int64_t r = u / oct, c = (u - r * oct) * 8;
-        const int n = (int)min((int64_t)8, p.cols - c);
-        const uint8_t* src = p.q + r * p.ld_q + c;
-        uint32_t w[2] = {0u, 0u};
-        if (p.vq && n == 8) {
-            const uint2 t = __ldcs(reinterpret_cast<const uint2*>(src));
-            w[0] = t.x, w[1] = t.y;
+    const int lane = threadIdx.x & 31;
+    const int64_t per_row = (p.cols + 256 * N - 1) / (256 * N), units = p.rows * per_row;
+    const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+    for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < units; u += warps) {
+        const Unit at = unit_of<N>(u, units, per_row);
+        const uint8_t* q = p.q + at.r * p.ld_q;
+        const float* sr = p.s + (brows == 1 ? at.r : at.r >> 7) * p.ld_s;
+        uint32_t w[N][2];
+        float s[N];
+        Eight<T> y8[N];
+        if (p.vq && whole_groups<N>(at.c0, 256, p.cols)) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int64_t c = at.c0 + 256 * i + 8 * lane;
+                const uint2 t = __ldcs(reinterpret_cast<const uint2*>(q + c));
+                w[i][0] = t.x, w[i][1] = t.y;
+                s[i] = __ldg(sr + (c >> p.qshift));
+            }
         } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k < n) w[k >> 2] |= (uint32_t)src[k] << (8 * (k & 3));
-        }
-        const float s = __ldg(p.s + (r / brows) * p.ld_s + c / p.qblock);
-        float a[4], b[4], v[8];
-        C::decode4(w[0], a);
-        C::decode4(w[1], b);
+            for (int i = 0; i < N; ++i) {
+                const int64_t c = at.c0 + 256 * i + 8 * lane;
+                w[i][0] = w[i][1] = 0u, s[i] = 0.f;
+                if (c < p.cols) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = a[k] * s, v[4 + k] = b[k] * s;
-        store8(y + r * p.ld_x + c, n, p.vx, v);
+                    for (int k = 0; k < 8; ++k)
+                        if (c + k < p.cols) w[i][k >> 2] |= (uint32_t)q[c + k] << (8 * (k & 3));
+                    s[i] = __ldg(sr + (c >> p.qshift));
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float a[4], b[4], v[8];
+            C::decode4(w[i][0], a);
+            C::decode4(w[i][1], b);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = a[k] * s[i], v[4 + k] = b[k] * s[i];
+            y8[i].set(v);
+        }
+        store_groups<T, N>(y + at.r * p.ld_x, at.c0, 256, p.cols, p.vx, y8);
     }
 }
 
@@ -157,18 +192,29 @@ QuantParams make_params(const void* v, int64_t rows, int64_t cols, int64_t ld, h
     p.s = const_cast<float*>(s);
     p.ld_s = ld_s;
     p.qblock = bcols;
+    p.qshift = bcols == 32 ? 5 : bcols == 64 ? 6 : bcols == 128 ? 7 : 8;
     p.vx = (uintptr_t)v % 16 == 0 && (ld * es) % 16 == 0;
     p.vq = (uintptr_t)q % 8 == 0 && ld_q % 8 == 0;
     return p;
 }
 
+// Grid of warps that share `rows` rows in units of `width` coordinates.
+unsigned unit_grid(int64_t rows, int64_t cols, int64_t width) {
+    const int64_t units = rows * ((cols + width - 1) / width);
+    return (unsigned)std::min<int64_t>((units + kThreads / 32 - 1) / (kThreads / 32), 32 * (int64_t)harp_sm_count());
+}
+
+// Units of four groups (1,024 coordinates: one lane's divisions serve 32 blocks of 32) where rows are long and
+// there are enough units for every SM; else of one.
+bool long_units(const QuantParams& p) {
+    return p.cols > 512 && p.rows * ((p.cols + 1023) / 1024) >= 16 * (int64_t)harp_sm_count();
+}
+
 template <typename T, typename C>
 harp_status run_quantize(const QuantParams& p, int32_t brows, cudaStream_t stream) {
     if (brows == 1) {
-        const int64_t units = p.rows * ((p.cols + 255) / 256);
-        const int64_t blocks = (units + kThreads / 32 - 1) / (kThreads / 32);
-        quantize_rows_kernel<T, C><<<(unsigned)std::min<int64_t>(blocks, 16 * (int64_t)harp_sm_count()), kThreads, 0,
-                                     stream>>>(p);
+        if (long_units(p)) quantize_rows_kernel<T, C, 4><<<unit_grid(p.rows, p.cols, 1024), kThreads, 0, stream>>>(p);
+        else quantize_rows_kernel<T, C, 1><<<unit_grid(p.rows, p.cols, 256), kThreads, 0, stream>>>(p);
     } else {
         const int64_t tiles = ((p.rows + 127) / 128) * ((p.cols + 127) / 128);
         if (tiles > 0x7fffffffll) return harp_fail(HARP_ERR_INVALID_ARG, "too many tiles");
@@ -182,10 +228,8 @@ harp_status run_quantize(const QuantParams& p, int32_t brows, cudaStream_t strea
 
 template <typename T, typename C>
 harp_status run_dequantize(const QuantParams& p, T* y, int32_t brows, cudaStream_t stream) {
-    const int64_t units = p.rows * ((p.cols + 7) / 8);
-    const int64_t blocks = (units + kThreads - 1) / kThreads;
-    dequantize_kernel<T, C><<<(unsigned)std::min<int64_t>(blocks, 32 * (int64_t)harp_sm_count()), kThreads, 0, stream>>>(
-        p, y, brows);
+    if (long_units(p)) dequantize_kernel<T, C, 4><<<unit_grid(p.rows, p.cols, 1024), kThreads, 0, stream>>>(p, y, brows);
+    else dequantize_kernel<T, C, 1><<<unit_grid(p.rows, p.cols, 256), kThreads, 0, stream>>>(p, y, brows);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return harp_fail(HARP_ERR_CUDA, cudaGetErrorString(e));
     harp_set_last_kernel("dequantize_kernel");

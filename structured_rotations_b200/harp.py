@@ -178,6 +178,7 @@ def _ld(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
+_CODE_DTYPE = {}   # code -> torch dtype, filled on first use
 _CODE = {"int8": HARP_CODE_I8, "e4m3": HARP_CODE_E4M3}
 
 
@@ -188,8 +189,11 @@ def _code(name: str) -> int:
 
 
 def _code_dtype(code: int):
-    import torch
-    return torch.int8 if code == HARP_CODE_I8 else torch.float8_e4m3fn
+    """The tensor type that holds codes of this format."""
+    if not _CODE_DTYPE:
+        import torch
+        _CODE_DTYPE.update({HARP_CODE_I8: torch.int8, HARP_CODE_E4M3: torch.float8_e4m3fn})
+    return _CODE_DTYPE[code]
 
 
 def _code_of(q) -> int:
@@ -202,15 +206,40 @@ def _code_of(q) -> int:
     raise TypeError(f"codes are int8 or float8_e4m3fn tensors, not {q.dtype}")
 
 
-def _expect(t, shape, dtype, what: str):
-    """t is a CUDA tensor of the current device with this shape and type and contiguous rows."""
-    if tuple(t.shape) != tuple(shape):
+def _expect(t, shape, dtype, dev: int, what: str):
+    """(address, leading dimension) of a 2-D tensor (address alone of a 1-D one), which must be on the CUDA
+    device dev with this shape and type and contiguous rows.  One pass over the tensor's attributes:
+    calls of a few microseconds spend most of their time here."""
+    if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
-    import torch
-    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
+    if t.get_device() != dev:
         raise ValueError(f"{what} must be on the current CUDA device, not {t.device}")
+    st = t.stride()
+    if len(st) == 1:
+        if st[0] != 1 and shape[0] > 1:
+            raise ValueError(f"{what} must be contiguous")
+        return t.data_ptr()
+    if st[1] != 1 and shape[1] > 1:
+        raise ValueError(f"the rows of {what} must be contiguous (stride(1) == 1)")
+    return t.data_ptr(), (st[0] if shape[0] > 1 else max(st[0], shape[1]))
+
+
+def _device(t, what: str) -> int:
+    """The current CUDA device, which must be t's."""
+    import torch
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{what} must be on the current CUDA device, not {t.device}")
+    return dev
+
+
+def _rows_of(t, what: str):
+    s = t.shape
+    if len(s) != 2:
+        raise ValueError(f"{what} must be a 2-D tensor")
+    return s
 
 
 def _cdiv(a: int, b: int) -> int:
@@ -302,14 +331,16 @@ class Plan:
             q = torch.empty(rows, self.d, dtype=_code_dtype(fmt), device=x.device)
         if scales is None:
             scales = torch.empty(rows, max(1, self.d // qblock), dtype=torch.float32, device=x.device)
-        if code == "e4m3":
-            _expect(x, (rows, self.d), x.dtype, "x")
-            _expect(q, (rows, self.d), torch.float8_e4m3fn, "q")
-            _expect(scales, (rows, max(1, self.d // qblock)), torch.float32, "scales")
+        if fmt == HARP_CODE_E4M3:
+            dev = _device(x, "x")
+            xp, ldx = _expect(x, (rows, self.d), x.dtype, dev, "x")
+            qp, ldq = _expect(q, (rows, self.d), torch.float8_e4m3fn, dev, "q")
+            sp, lds = _expect(scales, (rows, max(1, self.d // qblock)), torch.float32, dev, "scales")
+        else:
+            xp, ldx, qp, ldq, sp, lds = x.data_ptr(), _ld(x), q.data_ptr(), _ld(q), scales.data_ptr(), _ld(scales)
         d = HARP_FORWARD if direction == "forward" else HARP_INVERSE
-        _check(lib().harp_apply_quant_ex(self._h, x.data_ptr(), rows, _ld(x), _dtype_code(x), fmt, q.data_ptr(),
-                                         _ld(q), scales.data_ptr(), _ld(scales), qblock, d, _stream_handle(stream)),
-               "harp_apply_quant")
+        _check(lib().harp_apply_quant_ex(self._h, xp, rows, ldx, _dtype_code(x), fmt, qp, ldq, sp, lds, qblock, d,
+                                         _stream_handle(stream)), "harp_apply_quant")
         return q, scales
 
     def grad_workspace(self, device=None):
@@ -334,24 +365,22 @@ class Plan:
             qblock = self.d // nb
         if qblock not in (32, 64, 128, 256):
             raise ValueError("qblock must be 32, 64, 128 or 256")
-        code = _code_of(q)
-        _expect(q, (rows, self.d), q.dtype, "q")
-        _expect(scales, (rows, _cdiv(self.d, qblock)), torch.float32, "scales")
+        code, dev = _code_of(q), _device(q, "q")
+        qp, ldq = _expect(q, (rows, self.d), q.dtype, dev, "q")
+        sp, lds = _expect(scales, (rows, _cdiv(self.d, qblock)), torch.float32, dev, "scales")
         gt = _dtype_code(g)
-        _expect(g, (rows, self.d), g.dtype, "g")
+        gp, ldg = _expect(g, (rows, self.d), g.dtype, dev, "g")
         n = theta_count(self.schedule) if not getattr(self, "composite", False) else 1
         if dtheta is None:
             dtheta = torch.empty(n, dtype=torch.float32, device=q.device)
-        elif not dtheta.is_contiguous():
-            raise ValueError(f"dtheta must be a contiguous float32 tensor of {n} entries")
-        _expect(dtheta, (n,), torch.float32, "dtheta")
+        tp = _expect(dtheta, (n,), torch.float32, dev, "dtheta")
         if workspace is None:
             workspace = self.grad_workspace(q.device)
-        elif not workspace.is_contiguous() or not workspace.is_cuda or workspace.device != q.device:
-            raise ValueError("workspace must be contiguous, on the rows' device")
-        _check(lib().harp_grad_theta_quant(self._h, q.data_ptr(), _ld(q), code, scales.data_ptr(), _ld(scales), qblock,
-                                           g.data_ptr(), _ld(g), gt, rows, dtheta.data_ptr(), workspace.data_ptr(),
-                                           workspace.numel() * workspace.element_size(), _stream_handle(stream)),
+        elif not workspace.is_contiguous() or workspace.get_device() != dev:
+            raise ValueError("workspace must be contiguous, on the current CUDA device")
+        _check(lib().harp_grad_theta_quant(self._h, qp, ldq, code, sp, lds, qblock, gp, ldg, gt, rows, tp,
+                                           workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                           _stream_handle(stream)),
                "harp_grad_theta_quant")
         return dtheta
 
@@ -542,23 +571,21 @@ def quantize(x, block=(1, 128), code: str = "e4m3", q=None, scales=None, stream=
     e4m3 with 128: matmul_quant's row operand), (128, 128) for a weight (matmul_quant's).
     Returns (q, scales).  A new q has rows a multiple of 16 bytes apart."""
     import torch
-    fmt = _code(code)
-    if x.dim() != 2:
-        raise ValueError("expected a 2-D tensor of rows")
-    rows, cols = x.shape
-    dt = _dtype_code(x)
-    _expect(x, (rows, cols), x.dtype, "x")
+    fmt, dev = _code(code), _device(x, "x")
+    rows, cols = _rows_of(x, "x")
+    dt, qt = _dtype_code(x), _code_dtype(fmt)
+    xp, ldx = _expect(x, (rows, cols), x.dtype, dev, "x")
     br, bc = int(block[0]), int(block[1])
     if br < 1 or bc < 1:
         raise ValueError("blocks are (1, 32 | 64 | 128 | 256) or (128, 128)")
     if q is None:
-        q = torch.empty(rows, _cdiv(cols, 16) * 16, dtype=_code_dtype(fmt), device=x.device)[:, :cols]
+        q = torch.empty(rows, _cdiv(cols, 16) * 16, dtype=qt, device=x.device)[:, :cols]
     if scales is None:
         scales = torch.empty(_cdiv(rows, br), _cdiv(cols, bc), dtype=torch.float32, device=x.device)
-    _expect(q, (rows, cols), _code_dtype(fmt), "q")
-    _expect(scales, (_cdiv(rows, br), _cdiv(cols, bc)), torch.float32, "scales")
-    _check(lib().harp_quantize(x.data_ptr(), rows, cols, _ld(x), dt, fmt, br, bc, q.data_ptr(), _ld(q),
-                               scales.data_ptr(), _ld(scales), _stream_handle(stream)), "harp_quantize")
+    qp, ldq = _expect(q, (rows, cols), qt, dev, "q")
+    sp, lds = _expect(scales, (_cdiv(rows, br), _cdiv(cols, bc)), torch.float32, dev, "scales")
+    _check(lib().harp_quantize(xp, rows, cols, ldx, dt, fmt, br, bc, qp, ldq, sp, lds, _stream_handle(stream)),
+           "harp_quantize")
     return q, scales
 
 
@@ -566,10 +593,9 @@ def dequantize(q, scales, block=(1, 128), out=None, dtype=None, stream=None):
     """The values q * scale of quantize's codes (harp_dequantize), rounded to out's type (a new tensor
     of `dtype`, bfloat16 by default).  Returns out."""
     import torch
-    code = _code_of(q)
-    if q.dim() != 2:
-        raise ValueError("expected a 2-D tensor of codes")
-    rows, cols = q.shape
+    code, dev = _code_of(q), _device(q, "q")
+    rows, cols = _rows_of(q, "q")
+    qp, ldq = _expect(q, (rows, cols), q.dtype, dev, "q")
     br, bc = int(block[0]), int(block[1])
     if br < 1 or bc < 1:
         raise ValueError("blocks are (1, 32 | 64 | 128 | 256) or (128, 128)")
@@ -577,12 +603,11 @@ def dequantize(q, scales, block=(1, 128), out=None, dtype=None, stream=None):
         out = torch.empty(rows, cols, dtype=dtype or torch.bfloat16, device=q.device)
     elif dtype is not None and out.dtype != dtype:
         raise TypeError("out has another dtype")
+    sp, lds = _expect(scales, (_cdiv(rows, br), _cdiv(cols, bc)), torch.float32, dev, "scales")
     dt = _dtype_code(out)
-    _expect(q, (rows, cols), q.dtype, "q")
-    _expect(scales, (_cdiv(rows, br), _cdiv(cols, bc)), torch.float32, "scales")
-    _expect(out, (rows, cols), out.dtype, "out")
-    _check(lib().harp_dequantize(q.data_ptr(), _ld(q), scales.data_ptr(), _ld(scales), code, br, bc, rows, cols,
-                                 out.data_ptr(), _ld(out), dt, _stream_handle(stream)), "harp_dequantize")
+    yp, ldy = _expect(out, (rows, cols), out.dtype, dev, "out")
+    _check(lib().harp_dequantize(qp, ldq, sp, lds, code, br, bc, rows, cols, yp, ldy, dt, _stream_handle(stream)),
+           "harp_dequantize")
     return out
 
 
@@ -595,37 +620,33 @@ def rms_norm_quant(x, weight=None, residual=None, eps: float = 1e-6, qblock: int
     float8_e4m3fn), float32 scales [rows, ceil(d / qblock)], and the sum (x itself without a
     residual, unless h is given)."""
     import torch
-    fmt = _code(code)
-    if x.dim() != 2:
-        raise ValueError("expected a 2-D tensor of rows")
-    rows, d = x.shape
-    dt = _dtype_code(x)
+    fmt, dev = _code(code), _device(x, "x")
+    rows, d = shape = _rows_of(x, "x")
+    dt, t = _dtype_code(x), x.dtype
     if qblock not in (32, 64, 128, 256):
         raise ValueError("qblock must be 32, 64, 128 or 256")
-    _expect(x, (rows, d), x.dtype, "x")
+    xp, ldx = _expect(x, shape, t, dev, "x")
+    rp = wp = hp = yp = None
+    ldr = ldh = ldy = 0
     if residual is not None:
-        _expect(residual, (rows, d), x.dtype, "residual")
+        rp, ldr = _expect(residual, shape, t, dev, "residual")
         if h is None:
-            h = torch.empty(rows, d, dtype=x.dtype, device=x.device)
+            h = torch.empty(rows, d, dtype=t, device=x.device)
     if weight is not None:
-        _expect(weight, (d,), x.dtype, "weight")
-        if d > 1 and weight.stride(0) != 1:
-            raise ValueError("weight must be contiguous")
+        wp = _expect(weight, (d,), t, dev, "weight")
     if h is not None:
-        _expect(h, (rows, d), x.dtype, "h")
+        hp, ldh = _expect(h, shape, t, dev, "h")
     if y is not None:
-        _expect(y, (rows, d), x.dtype, "y")
+        yp, ldy = _expect(y, shape, t, dev, "y")
+    qt, nb = _code_dtype(fmt), _cdiv(d, qblock)
     if q is None:
-        q = torch.empty(rows, _cdiv(d, 16) * 16, dtype=_code_dtype(fmt), device=x.device)[:, :d]
+        q = torch.empty(rows, _cdiv(d, 16) * 16, dtype=qt, device=x.device)[:, :d]
     if scales is None:
-        scales = torch.empty(rows, _cdiv(d, qblock), dtype=torch.float32, device=x.device)
-    _expect(q, (rows, d), _code_dtype(fmt), "q")
-    _expect(scales, (rows, _cdiv(d, qblock)), torch.float32, "scales")
-    _check(lib().harp_rms_norm_quant(
-        x.data_ptr(), _ld(x), None if residual is None else residual.data_ptr(), 0 if residual is None else _ld(residual),
-        None if weight is None else weight.data_ptr(), rows, d, dt, float(eps), None if h is None else h.data_ptr(),
-        0 if h is None else _ld(h), None if y is None else y.data_ptr(), 0 if y is None else _ld(y), fmt, qblock,
-        q.data_ptr(), _ld(q), scales.data_ptr(), _ld(scales), _stream_handle(stream)), "harp_rms_norm_quant")
+        scales = torch.empty(rows, nb, dtype=torch.float32, device=x.device)
+    qp, ldq = _expect(q, shape, qt, dev, "q")
+    sp, lds = _expect(scales, (rows, nb), torch.float32, dev, "scales")
+    _check(lib().harp_rms_norm_quant(xp, ldx, rp, ldr, wp, rows, d, dt, eps, hp, ldh, yp, ldy, fmt, qblock, qp, ldq,
+                                     sp, lds, _stream_handle(stream)), "harp_rms_norm_quant")
     return q, scales, x if h is None else h
 
 
@@ -636,24 +657,23 @@ def matmul_quant(xq, xs, wq, ws, out=None, dtype=None, stream=None):
     dimensions that are multiples of 16, as quantize and apply_quant make them, run on the tensor
     cores.  Returns out."""
     import torch
-    if xq.dim() != 2 or wq.dim() != 2:
-        raise ValueError("expected 2-D tensors of codes")
-    rows, k = xq.shape
-    n = wq.shape[0]
-    f8 = torch.float8_e4m3fn
-    _expect(xq, (rows, k), f8, "xq")
-    _expect(wq, (n, k), f8, "wq")
-    _expect(xs, (rows, _cdiv(k, 128)), torch.float32, "xs")
-    _expect(ws, (_cdiv(n, 128), _cdiv(k, 128)), torch.float32, "ws")
+    rows, k = xshape = _rows_of(xq, "xq")
+    n, kw = _rows_of(wq, "wq")
+    f8, f32, dev, kb = torch.float8_e4m3fn, torch.float32, _device(xq, "xq"), _cdiv(k, 128)
+    if kw != k:
+        raise ValueError(f"wq must have {k} columns as xq, not {kw}")
+    xp, ldx = _expect(xq, xshape, f8, dev, "xq")
+    wp, ldw = _expect(wq, (n, k), f8, dev, "wq")
+    sp, lds = _expect(xs, (rows, kb), f32, dev, "xs")
+    vp, ldv = _expect(ws, (_cdiv(n, 128), kb), f32, dev, "ws")
     if out is None:
         out = torch.empty(rows, n, dtype=dtype or torch.bfloat16, device=xq.device)
     elif dtype is not None and out.dtype != dtype:
         raise TypeError("out has another dtype")
     dt = _dtype_code(out)
-    _expect(out, (rows, n), out.dtype, "out")
-    _check(lib().harp_matmul_quant(xq.data_ptr(), _ld(xq), xs.data_ptr(), _ld(xs), wq.data_ptr(), _ld(wq),
-                                   ws.data_ptr(), _ld(ws), rows, n, k, out.data_ptr(), _ld(out), dt,
-                                   _stream_handle(stream)), "harp_matmul_quant")
+    yp, ldy = _expect(out, (rows, n), out.dtype, dev, "out")
+    _check(lib().harp_matmul_quant(xp, ldx, sp, lds, wp, ldw, vp, ldv, rows, n, k, yp, ldy, dt, _stream_handle(stream)),
+           "harp_matmul_quant")
     return out
 
 
