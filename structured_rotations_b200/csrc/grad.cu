@@ -151,44 +151,53 @@ __device__ void load_tile_codes(const GradParams& p, float* A, float* H, int64_t
     const T* g = (const T*)p.g;
     constexpr int U = 4;                // groups of 8 in flight per thread
     const int cpr = (d + 7) / 8, total = nr * cpr;
-    for (int q0 = threadIdx.x; q0 < total; q0 += kThreads * U) {
-        uint2 code[U];
-        float s[U], fg[U][8];
+    auto put = [&](int q, const uint2& code, float s, const float (&fg)[8]) {
+        const int r = q / cpr, c = 8 * (q - r * cpr), n = min(8, d - c);
+        float lo[4], hi[4];
+        C::decode4(code.x, lo);
+        C::decode4(code.y, hi);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int q = q0 + u * kThreads;
-            if (q < total) {
-                const int r = q / cpr, c = 8 * (q - r * cpr), n = min(8, d - c);
-                const uint8_t* src = x + (row0 + r) * p.ld_x + c;
-                if (p.vec && n == 8) {
-                    code[u] = __ldg(reinterpret_cast<const uint2*>(src));
-                } else {
-                    uint32_t w[2] = {0u, 0u};
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (k < n) w[k >> 2] |= (uint32_t)src[k] << (8 * (k & 3));
-                    code[u] = make_uint2(w[0], w[1]);
-                }
-                s[u] = __ldg(p.xs + (row0 + r) * p.ld_xs + c / p.qblock);
-                harp_codes::load8(g + (row0 + r) * p.ld_g + c, n, p.vec, fg[u]);
+        for (int k = 0; k < 8; ++k) {
+            if (k < n) {
+                A[r * rs + swz(c + k)] = (k < 4 ? lo[k & 3] : hi[k & 3]) * s;
+                H[r * rs + swz(c + k)] = fg[k];
             }
         }
+    };
+    if (p.vec && (d & 7) == 0) {
+        for (int q0 = threadIdx.x; q0 < total; q0 += kThreads * U) {
+            uint2 code[U];
+            float s[U];
+            harp_codes::Eight<T> g8[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int q = q0 + u * kThreads;
-            if (q < total) {
-                const int r = q / cpr, c = 8 * (q - r * cpr), n = min(8, d - c);
-                float lo[4], hi[4];
-                C::decode4(code[u].x, lo);
-                C::decode4(code[u].y, hi);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    if (k < n) {
-                        A[r * rs + swz(c + k)] = (k < 4 ? lo[k & 3] : hi[k & 3]) * s[u];
-                        H[r * rs + swz(c + k)] = fg[u][k];
-                    }
+            for (int u = 0; u < U; ++u) {
+                const int q = q0 + u * kThreads;
+                if (q < total) {
+                    const int r = q / cpr, c = 8 * (q - r * cpr);
+                    code[u] = __ldcs(reinterpret_cast<const uint2*>(x + (row0 + r) * p.ld_x + c));
+                    s[u] = __ldg(p.xs + (row0 + r) * p.ld_xs + c / p.qblock);
+                    g8[u].load(g + (row0 + r) * p.ld_g + c);
                 }
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int q = q0 + u * kThreads;
+                float fg[8];
+                g8[u].get(fg);
+                if (q < total) put(q, code[u], s[u], fg);
+            }
+        }
+    } else {
+        for (int q = threadIdx.x; q < total; q += kThreads) {
+            const int r = q / cpr, c = 8 * (q - r * cpr), n = min(8, d - c);
+            const uint8_t* src = x + (row0 + r) * p.ld_x + c;
+            uint32_t w[2] = {0u, 0u};
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < n) w[k >> 2] |= (uint32_t)src[k] << (8 * (k & 3));
+            float fg[8];
+            harp_codes::load8(g + (row0 + r) * p.ld_g + c, n, false, fg);
+            put(q, make_uint2(w[0], w[1]), __ldg(p.xs + (row0 + r) * p.ld_xs + c / p.qblock), fg);
         }
     }
 }

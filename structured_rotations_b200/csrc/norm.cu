@@ -104,17 +104,20 @@ __global__ void __launch_bounds__(MOST) rms_norm_quant_kernel(const __grid_const
                 if (c + k >= p.d) v[k] = 0.f;
         }
     };
+    float v[N][8];   // kept: computing u again for the codes took 0.24 ms instead of 0.21 (with a weight, d = 5120)
+#pragma unroll
+    for (int i = 0; i < N; ++i) u(i, v[i]);
+    auto kept = [&](int i, float(&o)[8]) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = v[i][k];
+    };
     if (p.y) {
         Eight<T> y8[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float v[8];
-            u(i, v);
-            y8[i].set(v);
-        }
+        for (int i = 0; i < N; ++i) y8[i].set(v[i]);
         store_groups<T, N>((T*)p.y + r * p.ld_y, c0, step, p.d, p.vy, y8);
     }
-    if (p.q) quantize_groups<C, N>(u, c0, step, p.d, p.qblock / 8, p.q + r * p.ld_q, p.vq, p.s + r * p.ld_s);
+    if (p.q) quantize_groups<C, N>(kept, c0, step, p.d, p.qblock / 8, p.q + r * p.ld_q, p.vq, p.s + r * p.ld_s);
 }
 
 template <typename T, typename C>
