@@ -344,16 +344,19 @@ struct StageOffsets {
     int64_t off[HARP_MAX_STAGES];
 };
 
-// dL/dB -> dL/dtheta, one thread per block, in double.
+// dL/dB -> dL/dtheta in double, eight lanes per block: lane i holds row i of every matrix in
+// registers, and rows go round by shuffles (one thread per block, its matrices in local memory, took
+// 0.12 ms whatever the batch).
 __global__ void harp_grad_theta_kernel(PlanDesc pd, const float* __restrict__ theta_f32,
                                        const int8_t* __restrict__ theta_i8, const float* __restrict__ scales,
                                        const double* __restrict__ mixers, const int8_t* __restrict__ signs,
                                        const float* __restrict__ acc, StageOffsets acc_off,
                                        float* __restrict__ dtheta, int64_t total_blocks) {
-    const int64_t gid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (gid >= total_blocks) return;
+    const int64_t gid = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 3;
+    const int i = threadIdx.x & 7;                  // this lane's row
+    const bool live = gid < total_blocks;
     int t = 0;
-    int64_t c = gid;
+    int64_t c = live ? gid : 0;
     while (t < pd.m - 1 && c >= pd.st[t].nblocks) {
         c -= pd.st[t].nblocks;
         ++t;
@@ -367,66 +370,95 @@ __global__ void harp_grad_theta_kernel(PlanDesc pd, const float* __restrict__ th
     };
     const float* pb = acc + acc_off.off[t] + c * b * b;
     const double* gm = mixers + sd.mixer_off;
-    // R = dL/dB G^T, with stage 0's sign on column l (the device blocks are B_0 diag(S))
-    double R[8][8];
-    for (int k = 0; k < b; ++k)
-        for (int j = 0; j < b; ++j) {
-            double v = 0.0;
-            for (int l = 0; l < b; ++l) {
-                double pkl = (double)pb[k * b + l];
-                if (t == 0 && signs[l + b * c] < 0) pkl = -pkl;
-                v += pkl * gm[j * b + l];
-            }
-            R[k][j] = v;
-        }
+    // R = dL/dB G^T, with stage 0's sign on column l (the device blocks are B_0 diag(S)); rows and
+    // columns from b on are zero
+    double row[8], R[8];
+#pragma unroll
+    for (int l = 0; l < 8; ++l) {
+        double v = i < b && l < b ? (double)pb[i * b + l] : 0.0;
+        if (t == 0 && l < b && signs[l + b * c] < 0) v = -v;
+        row[l] = v;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        double v = 0.0;
+#pragma unroll
+        for (int l = 0; l < 8; ++l)
+            if (j < b && l < b) v += row[l] * gm[j * b + l];
+        R[j] = v;
+    }
     float* out = dtheta + poff;
+    const unsigned all = 0xffu << (threadIdx.x & 24);   // this block's lanes, which take the same branches
     if (b == 2) {
         const double th = param(0), cs = cos(th), sn = sin(th);
-        out[0] = (float)(-R[0][0] * sn - R[0][1] * cs + R[1][0] * cs - R[1][1] * sn);
+        const double r10 = __shfl_sync(all, R[0], 1, 8), r11 = __shfl_sync(all, R[1], 1, 8);
+        if (live && i == 0) out[0] = (float)(-R[0] * sn - R[1] * cs + r10 * cs - r11 * sn);
         return;
     }
     // M = (I - A)^{-1} by Gauss-Jordan without pivoting (every leading principal minor of
-    // I - A, A skew, is a product of (1 + lambda^2) > 0), then Q = M (I + A).
-    double lhs[8][8], M[8][8], Q[8][8], E[8][8];
-    int k = 0;
-    for (int i = 0; i < b; ++i)
-        for (int j = 0; j < b; ++j) lhs[i][j] = (i == j) ? 1.0 : 0.0, M[i][j] = (i == j) ? 1.0 : 0.0;
-    for (int i = 0; i < b; ++i)
-        for (int j = i + 1; j < b; ++j, ++k) {
-            const double a = param(k);
-            lhs[i][j] = -a;
-            lhs[j][i] = a;
+    // I - A, A skew, is a product of (1 + lambda^2) > 0), then Q = M (I + A).  Rows from b on: identity.
+    double lhs[8], M[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        lhs[j] = M[j] = i == j ? 1.0 : 0.0;
+        if (i != j && i < b && j < b) {
+            const int lo = min(i, j), hi = max(i, j);
+            const double a = param(lo * b - lo * (lo + 1) / 2 + hi - lo - 1);   // pair (lo, hi) of the upper triangle
+            lhs[j] = i < j ? -a : a;
         }
-    for (int col = 0; col < b; ++col) {
-        const double inv = 1.0 / lhs[col][col];
-        for (int j = 0; j < b; ++j) lhs[col][j] *= inv, M[col][j] *= inv;
-        for (int r = 0; r < b; ++r) {
-            if (r == col) continue;
-            const double f = lhs[r][col];
-            if (f == 0.0) continue;
-            for (int j = 0; j < b; ++j) lhs[r][j] -= f * lhs[col][j], M[r][j] -= f * M[col][j];
+    }
+#pragma unroll
+    for (int col = 0; col < 8; ++col) {
+        const double inv = 1.0 / __shfl_sync(all, lhs[col], col, 8);
+        const double f = lhs[col];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const double pl = __shfl_sync(all, lhs[j], col, 8) * inv, pm = __shfl_sync(all, M[j], col, 8) * inv;
+            if (i == col) {
+                lhs[j] = pl, M[j] = pm;
+            } else {
+                lhs[j] -= f * pl, M[j] -= f * pm;
+            }
         }
     }
     // I + A = 2 I - (I - A); Q = M (I + A) = 2 M - I
-    for (int i = 0; i < b; ++i)
-        for (int j = 0; j < b; ++j) Q[i][j] = 2.0 * M[i][j] - (i == j ? 1.0 : 0.0);
-    // E = M^T R (Q + I)^T = M^T R (2 M)^T
-    double T1[8][8];
-    for (int i = 0; i < b; ++i)
-        for (int j = 0; j < b; ++j) {
-            double v = 0.0;
-            for (int l = 0; l < b; ++l) v += M[l][i] * R[l][j];
-            T1[i][j] = v;
+    // E = M^T R (Q + I)^T = M^T R (2 M)^T: T1 = M^T R first, lane i its row i
+    double T1[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) T1[j] = 0.0;
+#pragma unroll
+    for (int l = 0; l < 8; ++l) {
+        double mli = 0.0;   // M[l][i]
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const double v = __shfl_sync(all, M[j], l, 8);
+            if (j == i) mli = v;
         }
-    for (int i = 0; i < b; ++i)
-        for (int j = 0; j < b; ++j) {
-            double v = 0.0;
-            for (int l = 0; l < b; ++l) v += T1[i][l] * (Q[j][l] + (j == l ? 1.0 : 0.0));
-            E[i][j] = v;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) T1[j] += mli * __shfl_sync(all, R[j], l, 8);
+    }
+    double E[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        double v = 0.0;
+#pragma unroll
+        for (int l = 0; l < 8; ++l) {
+            const double q = 2.0 * __shfl_sync(all, M[l], j, 8) - (j == l ? 1.0 : 0.0);   // Q[j][l]
+            if (l < b) v += T1[l] * (q + (j == l ? 1.0 : 0.0));
         }
-    k = 0;
-    for (int i = 0; i < b; ++i)
-        for (int j = i + 1; j < b; ++j, ++k) out[k] = (float)(E[i][j] - E[j][i]);
+        E[j] = v;
+    }
+#pragma unroll
+    for (int j = 1; j < 8; ++j) {
+        // E[i][j] - E[j][i] for i < j: lane j hands over its E[i], a register that depends on the lane
+        double other = 0.0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const double v = __shfl_sync(all, E[k], j, 8);
+            if (k == i) other = v;
+        }
+        if (live && i < j && j < b) out[i * b - i * (i + 1) / 2 + j - i - 1] = (float)(E[j] - other);
+    }
 }
 
 int sms_of_current_device() {
@@ -543,7 +575,13 @@ harp_status grad_checked(harp_plan_t p, const void* x, const void* g, int64_t ro
     const int rs = (int)((d + 31) / 32 * 32);
     const int64_t per_row = 2 * (int64_t)rs * 4;
     const int64_t budget = 227 * 1024;
-    const int R = (int)std::min<int64_t>(kMaxTileRows, budget / per_row);
+    int R = (int)std::min<int64_t>(kMaxTileRows, budget / per_row);
+    if (R >= 1 && rows > 0) {
+        // the same number of rounds over the SMs in tiles as low as they may be: no SM waits for another's
+        // full tile (1,001 rows of d = 5120: two rounds of 4 rows instead of 5)
+        const int64_t sms = sms_of_current_device(), rounds = (rows + R * sms - 1) / (R * sms);
+        R = (int)((rows + rounds * sms - 1) / (rounds * sms));
+    }
     if (R < 1) return harp_fail(HARP_ERR_UNSUPPORTED, "a row is too long for the gradient kernel's tile");
 
     cudaStream_t s = (cudaStream_t)stream;
@@ -580,7 +618,7 @@ harp_status grad_checked(harp_plan_t p, const void* x, const void* g, int64_t ro
     int64_t total = 0;
     for (int t = 0; t < pd.m; ++t) total += pd.st[t].nblocks;
     const bool i8 = p->kind == HARP_THETA_I8;
-    harp_grad_theta_kernel<<<(unsigned)((total + 127) / 128), 128, 0, s>>>(
+    harp_grad_theta_kernel<<<(unsigned)((8 * total + 127) / 128), 128, 0, s>>>(
         pd, i8 ? nullptr : (const float*)p->d_theta, i8 ? (const int8_t*)p->d_theta : nullptr, p->d_scales,
         p->d_mixers, p->d_signs, acc, L.off, dtheta, total);
     e = cudaGetLastError();
