@@ -40,7 +40,7 @@ struct GradParams {
     const void* x;
     const void* g;
     int64_t rows, ld_x, ld_g;
-    float* acc;                           // dL/dB accumulators, stage t at acc + acc_off[t], [c][k][l]
+    float* acc;                           // dL/dB accumulators, stage t at acc + acc_off[t] (acc_index)
     int64_t acc_off[HARP_MAX_STAGES];
     int R;                                // rows per tile
     int rs;                               // row stride of the shared-memory tiles (floats)
@@ -221,6 +221,23 @@ __device__ __forceinline__ void load_block(const float* lanes, int64_t c, float 
     }
 }
 
+// Entry e of block c in a stage's accumulator: like the lane-interleaved blocks (groups of 32 blocks, 16-byte
+// pieces or floats of a group's blocks side by side), so that a warp's atomic additions cover contiguous
+// bytes; the blocks behind the last whole group lie one after the other, and the size stays the blocks'.
+template <int BB>
+__device__ __forceinline__ int64_t acc_index(int64_t c, int e, int64_t nb) {
+    const int64_t grp = c >> 5, lane = c & 31;
+    if (c >= (nb & ~(int64_t)31)) return c * BB + e;
+    if (BB % 4 == 0) return ((grp * (BB / 4) + (e >> 2)) * 32 + lane) * 4 + (e & 3);
+    return (grp * BB + e) * 32 + lane;
+}
+__device__ __forceinline__ int64_t acc_index(int bb, int64_t c, int e, int64_t nb) {
+    const int64_t grp = c >> 5, lane = c & 31;
+    if (c >= (nb & ~(int64_t)31)) return c * bb + e;
+    if (bb % 4 == 0) return ((grp * (bb / 4) + (e >> 2)) * 32 + lane) * 4 + (e & 3);
+    return (grp * bb + e) * 32 + lane;
+}
+
 // Forward stage t on the activation tile: z <- M_t z.
 template <int B>
 __device__ void stage_forward(float* A, int nr, int rs, int64_t nb, int s, const float* lanes) {
@@ -284,14 +301,15 @@ __device__ void stage_backward(float* A, float* H, int nr, int rs, int64_t nb, i
                 h[off[l]] = hin;
             }
         }
-        float* dst = acc_t + c * BB;
+        float* dst = acc_t + acc_index<BB>(c, 0, nb);
+        const int step = c < (nb & ~(int64_t)31) ? (BB % 4 == 0 ? 128 : 32) : (BB % 4 == 0 ? 4 : 1);
         if constexpr (BB % 4 == 0) {
 #pragma unroll
             for (int e = 0; e < BB; e += 4)
-                atomicAdd(reinterpret_cast<float4*>(dst + e), make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]));
+                atomicAdd(reinterpret_cast<float4*>(dst + e / 4 * step), make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]));
         } else {
 #pragma unroll
-            for (int e = 0; e < BB; ++e) atomicAdd(dst + e, sum[e]);
+            for (int e = 0; e < BB; ++e) atomicAdd(dst + e * step, sum[e]);
         }
     }
 }
@@ -368,14 +386,14 @@ __global__ void harp_grad_theta_kernel(PlanDesc pd, const float* __restrict__ th
     auto param = [&](int k) -> double {
         return theta_i8 ? (double)theta_i8[poff + k] * scale : (double)theta_f32[poff + k];
     };
-    const float* pb = acc + acc_off.off[t] + c * b * b;
+    const float* pb = acc + acc_off.off[t];
     const double* gm = mixers + sd.mixer_off;
     // R = dL/dB G^T, with stage 0's sign on column l (the device blocks are B_0 diag(S)); rows and
     // columns from b on are zero
     double row[8], R[8];
 #pragma unroll
     for (int l = 0; l < 8; ++l) {
-        double v = i < b && l < b ? (double)pb[i * b + l] : 0.0;
+        double v = i < b && l < b ? (double)pb[acc_index(b * b, c, i * b + l, sd.nblocks)] : 0.0;
         if (t == 0 && l < b && signs[l + b * c] < 0) v = -v;
         row[l] = v;
     }
@@ -471,7 +489,7 @@ int sms_of_current_device() {
     return n;
 }
 
-// Accumulator layout: per stage nblocks * b * b floats, each stage starting on a 16-byte
+// Accumulators: per stage nblocks * b * b floats, each stage starting on a 16-byte
 // boundary (vector atomics).
 struct AccLayout {
     StageOffsets off = {};
