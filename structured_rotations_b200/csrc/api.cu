@@ -190,6 +190,11 @@ extern "C" harp_status harp_apply_quant_ex(harp_plan_t p, const void* x, int64_t
         harp_clear_error();
     }
     QuantOut qo{scales, ld_s, qblock, code};
+    if (code == HARP_CODE_E4M3 && (choice == kCluster || (choice == kAuto && rows < kClusterRows))) {
+        st = launch_apply_cluster(p, x, q, rows, ld_x, ld_q, HARP_BF16, HARP_BF16, dir, stream, &qo);
+        if (st != HARP_ERR_UNSUPPORTED || choice == kCluster) return st;
+        harp_clear_error();
+    }
     st = launch_apply_tiled(p, x, q, rows, ld_x, ld_q, HARP_BF16, HARP_BF16, dir, stream, &qo);
     if (st == HARP_ERR_UNSUPPORTED)
         return harp_fail(HARP_ERR_UNSUPPORTED, "the fused quantizer needs radices <= 8, d % 8 == 0, 16-byte "

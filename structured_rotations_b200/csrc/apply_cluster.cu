@@ -176,11 +176,15 @@ void cluster_state_free(harp_plan_s* p) {
 }
 
 harp_status launch_apply_cluster(const harp_plan_s* p, const void* x, void* y, int64_t rows, int64_t ld_x,
-                                 int64_t ld_y, harp_dtype in_dtype, harp_dtype out_dtype, harp_dir dir, void* stream) {
+                                 int64_t ld_y, harp_dtype in_dtype, harp_dtype out_dtype, harp_dir dir, void* stream,
+                                 const QuantOut* quant) {
     ClusterState* cs = static_cast<ClusterState*>(p->cluster);
     if (!cs) return HARP_ERR_UNSUPPORTED;
     if (in_dtype == HARP_F32 && out_dtype == HARP_BF16) return HARP_ERR_UNSUPPORTED;
-    const int64_t es_in = in_dtype == HARP_F32 ? 4 : 2, es_out = out_dtype == HARP_F32 ? 4 : 2;
+    // the quantizer's epilogue needs whole blocks in a CTA: the slabs in which the inverse ends
+    if (quant && (in_dtype != HARP_BF16 || quant->code != HARP_CODE_E4M3 || dir != HARP_INVERSE || cs->dl % quant->qblock))
+        return HARP_ERR_UNSUPPORTED;
+    const int64_t es_in = in_dtype == HARP_F32 ? 4 : 2, es_out = quant ? 1 : out_dtype == HARP_F32 ? 4 : 2;
     if (((uintptr_t)x & 15) || ((uintptr_t)y & 15) || ((ld_x * es_in) & 15) || ((ld_y * es_out) & 15))
         return HARP_ERR_UNSUPPORTED;
     const PlanDesc& pd = p->desc;
@@ -211,6 +215,9 @@ harp_status launch_apply_cluster(const harp_plan_s* p, const void* x, void* y, i
     cp.ld_y = ld_y;
     cp.R = (int)std::min<int64_t>(cs->r_max, (rows + 3) / 4 * 4);
     cp.status = p->d_status;
+    cp.scales = quant ? quant->scales : nullptr;
+    cp.ld_s = quant ? quant->ld_s : 0;
+    cp.qlanes = quant ? quant->qblock / 8 : 1;
     if (!cs->done.load(std::memory_order_acquire)) {
         // the table's build has finished once its event has (a poll, no wait)
         const cudaError_t q = cudaEventQuery(cs->built);
@@ -224,7 +231,9 @@ harp_status launch_apply_cluster(const harp_plan_s* p, const void* x, void* y, i
     cudaStream_t s = (cudaStream_t)stream;
     const bool inv = dir == HARP_INVERSE;
     cudaError_t e;
-    if (in_dtype == HARP_BF16 && out_dtype == HARP_BF16)
+    if (quant)
+        e = harp_cluster_launch_bf16_e4m3(cs->which, cs->cl, cp, smem, grid, s);
+    else if (in_dtype == HARP_BF16 && out_dtype == HARP_BF16)
         e = harp_cluster_launch_bf16(cs->which, cs->cl, inv, cp, smem, grid, s);
     else if (in_dtype == HARP_F32)
         e = harp_cluster_launch_f32(cs->which, cs->cl, inv, cp, smem, grid, s);

@@ -58,6 +58,9 @@ struct ClusterParams {
     int early;                            // the table is known complete: stage it before the
                                           // wait for the previous kernel of the stream
     int* status;
+    float* scales;                        // e4m3 codes in y: per-block scales, their row stride, and the
+    int64_t ld_s;                         // lanes (8 coordinates each) that hold a quantizer block
+    int qlanes;
 };
 
 // ----------------------------------------------------------------- PTX ---
@@ -214,6 +217,31 @@ __device__ __forceinline__ void drain(const ClusterParams& p, const float4* buf,
     }
 }
 
+// The same with the blockwise quantizer (harp_tiled::quant_rows): the inverse ends in slab order, where
+// a CTA holds dl consecutive coordinates, whole quantizer blocks; the lanes of a block are neighbours
+// (dl / 8 is a multiple of qlanes), and every lane of a warp takes the same trips.
+__device__ __forceinline__ void drain_quant(const ClusterParams& p, const float4* buf, int r, int64_t row0, int nr, int qv) {
+    const int d8 = p.dl / 8, total = qv * d8, lane = threadIdx.x & 31;
+    for (int e0 = (int)threadIdx.x - lane; e0 < total; e0 += kThreads) {
+        const int e8 = e0 + lane;
+        const unsigned mask = __ballot_sync(0xffffffffu, e8 < total);
+        if (e8 >= total) continue;
+        const int q = e8 / d8, jj = e8 - q * d8, jx = jj & 7;
+        const float4* st = buf + q * p.dl + 8 * jj;
+        float v[4][8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float4 t = st[k ^ jx];
+            v[0][k] = t.x, v[1][k] = t.y, v[2][k] = t.z, v[3][k] = t.w;
+        }
+        const int64_t row = row0 + 4 * q;
+        const int col = r * p.dl + 8 * jj;
+        harp_tiled::quant_rows<4>(v, min(4, nr - 4 * q), (__nv_fp8_e4m3*)p.y + row * p.ld_y + col, p.ld_y,
+                                  p.scales + row * p.ld_s + col / (8 * p.qlanes), p.ld_s, p.qlanes, mask,
+                                  (jj & (p.qlanes - 1)) == 0);
+    }
+}
+
 // Every coordinate of this CTA's `src` buffer (slab order if from_slab, else pencil order) to the
 // other phase's buffer `dst` of the CTA that owns it, by 8-coordinate runs (a run has one owner
 // and maps to one aligned run there, since P is a multiple of 8).  The stores are asynchronous
@@ -347,7 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1) harp_cluster_kernel(const __grid_
             }
         }
         have_blocks = true;
-        drain<TOut>(p, second, INV, (int)r, row0, nr, qv);
+        if constexpr (harp_tiled::is_code<TOut>) drain_quant(p, second, (int)r, row0, nr, qv);
+        else drain<TOut>(p, second, INV, (int)r, row0, nr, qv);
         cluster_arrive();   // this CTA's `second` buffer may take the next tile's exchange
     }
     cluster_wait();         // matches the last arrive
@@ -406,3 +435,6 @@ cudaError_t harp_cluster_launch_f32(int which, int cl, bool inverse, const harp_
                                     size_t smem, int grid, cudaStream_t stream);
 cudaError_t harp_cluster_launch_bf16_f32(int which, int cl, bool inverse, const harp_cluster::ClusterParams& cp,
                                          size_t smem, int grid, cudaStream_t stream);
+// bf16 rows in, e4m3 codes and scales out: the inverse only
+cudaError_t harp_cluster_launch_bf16_e4m3(int which, int cl, const harp_cluster::ClusterParams& cp, size_t smem, int grid,
+                                          cudaStream_t stream);

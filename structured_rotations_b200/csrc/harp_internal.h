@@ -107,10 +107,10 @@ void fast_state_free(harp_plan_s* p);
 void cluster_prepare(harp_plan_s* p, void* stream);
 void cluster_state_free(harp_plan_s* p);
 // Cluster row kernel (apply_cluster.cu): HARP_ERR_UNSUPPORTED for plans without a cluster
-// table, unaligned rows and fp32-in / bf16-out.
+// table, unaligned rows and fp32-in / bf16-out.  With `quant` (y: e4m3 codes) the inverse only.
 harp_status launch_apply_cluster(const harp_plan_s* p, const void* x, void* y, int64_t rows, int64_t ld_x,
                                  int64_t ld_y, harp_dtype in_dtype, harp_dtype out_dtype, harp_dir dir,
-                                 void* stream);
+                                 void* stream, const struct QuantOut* quant = nullptr);
 // Builds the specialized kernel's coefficient table (and its launch attributes) on
 // `stream` for plans it covers; a no-op for other plans.  Called by materialization, so
 // every later launch only reads the table.  A plan whose table cannot be built (no

@@ -115,3 +115,22 @@ def test_refusals_and_empty():
     with pytest.raises(HB.HarpError) as e:                      # code rows not 16-byte aligned
         gp.apply_quant(x, code="e4m3", q=torch.empty(4, 4104, dtype=torch.float8_e4m3fn, device=DEV)[:, :4096])
     assert e.value.status == HB.HARP_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("rows,qblock", [(1, 32), (4, 128), (16, 256), (33, 64), (64, 128)])
+def test_cluster_kernel_equals_the_tiled_one(monkeypatch, rows, qblock):
+    """Small batches of the inverse split each row over a cluster; the stage arithmetic is the tiled kernel's,
+    so codes and scales are the same bits, also in padded outputs, which stay as they were beside them."""
+    gp, _ = plans("d8192_int8")
+    x = to_dev(W.draw_encoded(W.get("d8192_int8"), 0, rows))
+    x[rows - 1, 100:] = 0
+    monkeypatch.setenv("HARP_KERNEL", "tiled")
+    q0, s0 = gp.apply_quant(x, qblock, "inverse", code="e4m3")
+    monkeypatch.delenv("HARP_KERNEL")
+    qp = torch.full((rows, 8192 + 16), 5, dtype=torch.uint8, device=DEV)
+    sp = torch.full((rows, 8192 // qblock + 1), -1.0, device=DEV)
+    gp.apply_quant(x, qblock, "inverse", q=qp[:, :8192].view(torch.float8_e4m3fn), scales=sp[:, : 8192 // qblock], code="e4m3")
+    assert H.last_kernel() == "harp_cluster_kernel"
+    assert torch.equal(qp[:, :8192], q0.view(torch.uint8)) and torch.equal(sp[:, : 8192 // qblock], s0)
+    assert torch.all(qp[:, 8192:] == 5) and torch.all(sp[:, 8192 // qblock:] == -1.0)
+    gp.device_status()
