@@ -211,7 +211,12 @@ extern "C" harp_status harp_matmul_quant(const void* x, int64_t ld_x, const floa
     const bool tma = ((uintptr_t)x | (uintptr_t)w | (uintptr_t)ld_x | (uintptr_t)ld_w) % 16 == 0 && ld_x < (1ll << 40) &&
                      ld_w < (1ll << 40);
     if (tma) {
-        const harp_status st = rows > 128 ? launch_matmul_tiles(p, out_dtype, stream) : launch_matmul_rows(p, out_dtype, stream);
+        // Up to 64 rows the weight's bytes count and the rows kernel streams them with every SM (64 x 28672 x
+        // 8192: 45 us against 67); from there the pair kernel multiplies faster (128 x 4096 x 4096: 14.7 us
+        // against 18.5), unless up to 128 rows meet so few columns that most pairs would idle while
+        // the rows kernel splits k (128 x 1024 x 8192: 13.4 us against 24.5).
+        const bool few = rows <= 64 || (rows <= 128 && (n + 127) / 128 <= harp_sm_count() / 8);
+        const harp_status st = few ? launch_matmul_rows(p, out_dtype, stream) : launch_matmul_tiles(p, out_dtype, stream);
         if (st != HARP_ERR_UNSUPPORTED) return st;
         harp_clear_error();
     }

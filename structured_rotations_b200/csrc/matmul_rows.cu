@@ -8,6 +8,9 @@
 // fp32 registers while the next blocks' products run.  With few weight tiles a cluster of C CTAs
 // splits k: each keeps the sums of its share, and they are added over distributed shared memory in
 // the order of the ranks, so that equal calls give equal bits.
+// Measured: 1 x 28672 x 8192 in 41 us, 5.7 TB/s of the weight's bytes (a copy: 6.5); 24 x 5120 x 5120 in 9.3
+// us, where the launch, the first loads and the sum over the cluster count; all scales of a CTA loaded
+// at its start instead of a block ahead: no faster.
 //   warps 0-3  sums: thread = one weight row (a lane of tensor memory), BT registers
 //   warp 4     TMA loads;  warp 5  tensor-memory allocation and tcgen05.mma
 #include <algorithm>
@@ -73,6 +76,10 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
     __syncthreads();
     fence_after();
     const uint32_t tmem = *slot;
+    // the prologue above ran beside the end of the stream's previous kernel, which may have made the
+    // operands; everything below comes after it
+    launch_dependents();
+    wait_previous_grid();
 
     float sum[BT];
 #pragma unroll
@@ -208,13 +215,15 @@ harp_status launch(const MatmulParams& p, cudaStream_t stream) {
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = S::kSmem;
         cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
+        cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = (unsigned)split;
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = 2;
         e = cudaLaunchKernelEx(&cfg, kern, mx, mw, p, split, status);
         if (e == cudaSuccess) e = cudaGetLastError();
     }

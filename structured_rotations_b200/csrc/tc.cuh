@@ -100,6 +100,11 @@ __device__ __forceinline__ void drain_delay() {
     while (clock64() - t0 < 4000000ll) __nanosleep(1000);
 }
 
+// Programmatic dependent launch: the next kernel of the stream may start its prologue / the previous
+// one has ended and its memory is visible.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // A box of a 2-D tensor map into this CTA's shared memory.
 __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
     asm volatile(
