@@ -216,11 +216,11 @@ def _expect(t, shape, dtype, dev: int, what: str):
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{what} must be on the current CUDA device, not {t.device}")
+    if t.is_contiguous():
+        return (t.data_ptr(), shape[1]) if len(shape) == 2 else t.data_ptr()
     st = t.stride()
     if len(st) == 1:
-        if st[0] != 1 and shape[0] > 1:
-            raise ValueError(f"{what} must be contiguous")
-        return t.data_ptr()
+        raise ValueError(f"{what} must be contiguous")
     if st[1] != 1 and shape[1] > 1:
         raise ValueError(f"the rows of {what} must be contiguous (stride(1) == 1)")
     return t.data_ptr(), (st[0] if shape[0] > 1 else max(st[0], shape[1]))
