@@ -198,11 +198,9 @@ def _code_dtype(code: int):
 
 def _code_of(q) -> int:
     """The code format of a tensor of codes, by its type."""
-    import torch
-    if q.dtype == torch.int8:
-        return HARP_CODE_I8
-    if q.dtype == torch.float8_e4m3fn:
-        return HARP_CODE_E4M3
+    for code in _CODE.values():
+        if q.dtype is _code_dtype(code):
+            return code
     raise TypeError(f"codes are int8 or float8_e4m3fn tensors, not {q.dtype}")
 
 
@@ -226,11 +224,23 @@ def _expect(t, shape, dtype, dev: int, what: str):
     return t.data_ptr(), (st[0] if shape[0] > 1 else max(st[0], shape[1]))
 
 
-def _device(t, what: str) -> int:
-    """The current CUDA device, which must be t's."""
-    import torch
+_TORCH = None   # (float8_e4m3fn, float32, current device, its current raw stream), filled on first use
+
+
+def _torch():
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        C = torch._C
+        raw = getattr(C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        _TORCH = (torch.float8_e4m3fn, torch.float32, C._cuda_getDevice, raw)
+    return _TORCH
+
+
+def _device(t, what: str, current) -> int:
+    """The current CUDA device (current()), which must be t's."""
     dev = t.get_device()
-    if dev < 0 or dev != torch._C._cuda_getDevice():
+    if dev < 0 or dev != current():
         raise ValueError(f"{what} must be on the current CUDA device, not {t.device}")
     return dev
 
@@ -332,7 +342,7 @@ class Plan:
         if scales is None:
             scales = torch.empty(rows, max(1, self.d // qblock), dtype=torch.float32, device=x.device)
         if fmt == HARP_CODE_E4M3:
-            dev = _device(x, "x")
+            dev = _device(x, "x", (_TORCH or _torch())[2])
             xp, ldx = _expect(x, (rows, self.d), x.dtype, dev, "x")
             qp, ldq = _expect(q, (rows, self.d), torch.float8_e4m3fn, dev, "q")
             sp, lds = _expect(scales, (rows, max(1, self.d // qblock)), torch.float32, dev, "scales")
@@ -365,7 +375,7 @@ class Plan:
             qblock = self.d // nb
         if qblock not in (32, 64, 128, 256):
             raise ValueError("qblock must be 32, 64, 128 or 256")
-        code, dev = _code_of(q), _device(q, "q")
+        code, dev = _code_of(q), _device(q, "q", (_TORCH or _torch())[2])
         qp, ldq = _expect(q, (rows, self.d), q.dtype, dev, "q")
         sp, lds = _expect(scales, (rows, _cdiv(self.d, qblock)), torch.float32, dev, "scales")
         gt = _dtype_code(g)
@@ -570,44 +580,46 @@ def quantize(x, block=(1, 128), code: str = "e4m3", q=None, scales=None, stream=
     for block = (b0, b1): (1, 32 | 64 | 128 | 256) for rows (checkpoints for Plan.grad_theta_quant;
     e4m3 with 128: matmul_quant's row operand), (128, 128) for a weight (matmul_quant's).
     Returns (q, scales).  A new q has rows a multiple of 16 bytes apart."""
-    import torch
-    fmt, dev = _code(code), _device(x, "x")
-    rows, cols = _rows_of(x, "x")
+    _, f32, current, raw = _TORCH or _torch()
+    fmt, dev = _code(code), _device(x, "x", current)
+    rows, cols = shape = _rows_of(x, "x")
     dt, qt = _dtype_code(x), _code_dtype(fmt)
-    xp, ldx = _expect(x, (rows, cols), x.dtype, dev, "x")
-    br, bc = int(block[0]), int(block[1])
+    xp, ldx = _expect(x, shape, x.dtype, dev, "x")
+    br, bc = block
     if br < 1 or bc < 1:
         raise ValueError("blocks are (1, 32 | 64 | 128 | 256) or (128, 128)")
+    sshape = (-(-rows // br), -(-cols // bc))
     if q is None:
-        q = torch.empty(rows, _cdiv(cols, 16) * 16, dtype=qt, device=x.device)[:, :cols]
+        q = x.new_empty((rows, _cdiv(cols, 16) * 16), dtype=qt)[:, :cols]
     if scales is None:
-        scales = torch.empty(_cdiv(rows, br), _cdiv(cols, bc), dtype=torch.float32, device=x.device)
-    qp, ldq = _expect(q, (rows, cols), qt, dev, "q")
-    sp, lds = _expect(scales, (_cdiv(rows, br), _cdiv(cols, bc)), torch.float32, dev, "scales")
-    _check(lib().harp_quantize(xp, rows, cols, ldx, dt, fmt, br, bc, qp, ldq, sp, lds, _stream_handle(stream)),
-           "harp_quantize")
+        scales = x.new_empty(sshape, dtype=f32)
+    qp, ldq = _expect(q, shape, qt, dev, "q")
+    sp, lds = _expect(scales, sshape, f32, dev, "scales")
+    _check(lib().harp_quantize(xp, rows, cols, ldx, dt, fmt, br, bc, qp, ldq, sp, lds,
+                               raw(dev) if stream is None else _stream_handle(stream)), "harp_quantize")
     return q, scales
 
 
 def dequantize(q, scales, block=(1, 128), out=None, dtype=None, stream=None):
     """The values q * scale of quantize's codes (harp_dequantize), rounded to out's type (a new tensor
     of `dtype`, bfloat16 by default).  Returns out."""
-    import torch
-    code, dev = _code_of(q), _device(q, "q")
-    rows, cols = _rows_of(q, "q")
-    qp, ldq = _expect(q, (rows, cols), q.dtype, dev, "q")
-    br, bc = int(block[0]), int(block[1])
+    _, f32, current, raw = _TORCH or _torch()
+    code, dev = _code_of(q), _device(q, "q", current)
+    rows, cols = shape = _rows_of(q, "q")
+    qp, ldq = _expect(q, shape, q.dtype, dev, "q")
+    br, bc = block
     if br < 1 or bc < 1:
         raise ValueError("blocks are (1, 32 | 64 | 128 | 256) or (128, 128)")
     if out is None:
+        import torch
         out = torch.empty(rows, cols, dtype=dtype or torch.bfloat16, device=q.device)
     elif dtype is not None and out.dtype != dtype:
         raise TypeError("out has another dtype")
-    sp, lds = _expect(scales, (_cdiv(rows, br), _cdiv(cols, bc)), torch.float32, dev, "scales")
+    sp, lds = _expect(scales, (-(-rows // br), -(-cols // bc)), f32, dev, "scales")
     dt = _dtype_code(out)
-    yp, ldy = _expect(out, (rows, cols), out.dtype, dev, "out")
-    _check(lib().harp_dequantize(qp, ldq, sp, lds, code, br, bc, rows, cols, yp, ldy, dt, _stream_handle(stream)),
-           "harp_dequantize")
+    yp, ldy = _expect(out, shape, out.dtype, dev, "out")
+    _check(lib().harp_dequantize(qp, ldq, sp, lds, code, br, bc, rows, cols, yp, ldy, dt,
+                                 raw(dev) if stream is None else _stream_handle(stream)), "harp_dequantize")
     return out
 
 
@@ -619,8 +631,8 @@ def rms_norm_quant(x, weight=None, residual=None, eps: float = 1e-6, qblock: int
     y, if given, u rounded to x's type.  Returns (q, scales, h): codes [rows, d] (int8 or
     float8_e4m3fn), float32 scales [rows, ceil(d / qblock)], and the sum (x itself without a
     residual, unless h is given)."""
-    import torch
-    fmt, dev = _code(code), _device(x, "x")
+    _, f32, current, raw = _TORCH or _torch()
+    fmt, dev = _code(code), _device(x, "x", current)
     rows, d = shape = _rows_of(x, "x")
     dt, t = _dtype_code(x), x.dtype
     if qblock not in (32, 64, 128, 256):
@@ -631,7 +643,7 @@ def rms_norm_quant(x, weight=None, residual=None, eps: float = 1e-6, qblock: int
     if residual is not None:
         rp, ldr = _expect(residual, shape, t, dev, "residual")
         if h is None:
-            h = torch.empty(rows, d, dtype=t, device=x.device)
+            h = x.new_empty(shape)
     if weight is not None:
         wp = _expect(weight, (d,), t, dev, "weight")
     if h is not None:
@@ -640,13 +652,14 @@ def rms_norm_quant(x, weight=None, residual=None, eps: float = 1e-6, qblock: int
         yp, ldy = _expect(y, shape, t, dev, "y")
     qt, nb = _code_dtype(fmt), _cdiv(d, qblock)
     if q is None:
-        q = torch.empty(rows, _cdiv(d, 16) * 16, dtype=qt, device=x.device)[:, :d]
+        q = x.new_empty((rows, _cdiv(d, 16) * 16), dtype=qt)[:, :d]
     if scales is None:
-        scales = torch.empty(rows, nb, dtype=torch.float32, device=x.device)
+        scales = x.new_empty((rows, nb), dtype=f32)
     qp, ldq = _expect(q, shape, qt, dev, "q")
-    sp, lds = _expect(scales, (rows, nb), torch.float32, dev, "scales")
+    sp, lds = _expect(scales, (rows, nb), f32, dev, "scales")
     _check(lib().harp_rms_norm_quant(xp, ldx, rp, ldr, wp, rows, d, dt, eps, hp, ldh, yp, ldy, fmt, qblock, qp, ldq,
-                                     sp, lds, _stream_handle(stream)), "harp_rms_norm_quant")
+                                     sp, lds, raw(dev) if stream is None else _stream_handle(stream)),
+           "harp_rms_norm_quant")
     return q, scales, x if h is None else h
 
 
@@ -656,24 +669,26 @@ def matmul_quant(xq, xs, wq, ws, out=None, dtype=None, stream=None):
     out [rows, n] in bfloat16 (the default) or float32.  Operands 16-byte aligned with leading
     dimensions that are multiples of 16, as quantize and apply_quant make them, run on the tensor
     cores.  Returns out."""
-    import torch
+    f8, f32, current, raw = _TORCH or _torch()
+    dev = _device(xq, "xq", current)
     rows, k = xshape = _rows_of(xq, "xq")
-    n, kw = _rows_of(wq, "wq")
-    f8, f32, dev, kb = torch.float8_e4m3fn, torch.float32, _device(xq, "xq"), _cdiv(k, 128)
+    n, kw = wshape = _rows_of(wq, "wq")
+    kb = -(-k // 128)
     if kw != k:
         raise ValueError(f"wq must have {k} columns as xq, not {kw}")
     xp, ldx = _expect(xq, xshape, f8, dev, "xq")
-    wp, ldw = _expect(wq, (n, k), f8, dev, "wq")
+    wp, ldw = _expect(wq, wshape, f8, dev, "wq")
     sp, lds = _expect(xs, (rows, kb), f32, dev, "xs")
-    vp, ldv = _expect(ws, (_cdiv(n, 128), kb), f32, dev, "ws")
+    vp, ldv = _expect(ws, (-(-n // 128), kb), f32, dev, "ws")
     if out is None:
+        import torch
         out = torch.empty(rows, n, dtype=dtype or torch.bfloat16, device=xq.device)
     elif dtype is not None and out.dtype != dtype:
         raise TypeError("out has another dtype")
     dt = _dtype_code(out)
     yp, ldy = _expect(out, (rows, n), out.dtype, dev, "out")
-    _check(lib().harp_matmul_quant(xp, ldx, sp, lds, wp, ldw, vp, ldv, rows, n, k, yp, ldy, dt, _stream_handle(stream)),
-           "harp_matmul_quant")
+    _check(lib().harp_matmul_quant(xp, ldx, sp, lds, wp, ldw, vp, ldv, rows, n, k, yp, ldy, dt,
+                                   raw(dev) if stream is None else _stream_handle(stream)), "harp_matmul_quant")
     return out
 
 
