@@ -154,6 +154,16 @@ def _stream_handle(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+def _on(stream):
+    """The context of a call on `stream` (a torch stream or a handle): what the call allocates belongs to
+    that stream, so its memory neither comes from work that another stream has still under way nor
+    goes to another stream before the call's kernels are done."""
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 _DTYPE = {"float32": HARP_F32, "bfloat16": HARP_BF16}
 
 
@@ -333,6 +343,9 @@ class Plan:
         [rows, d / qblock] out, y ~= q * scale per aligned block of qblock coordinates.
         Returns (q, scales); e4m3 codes in blocks of 128 are matmul_quant's row operand."""
         import torch
+        if stream is not None:
+            with _on(stream):
+                return self.apply_quant(x, qblock, direction, q, scales, None, code)
         if x.shape[-1] != self.d:
             raise ValueError(f"last dimension must be d={self.d}")
         fmt = _code(code)
@@ -347,10 +360,12 @@ class Plan:
             qp, ldq = _expect(q, (rows, self.d), torch.float8_e4m3fn, dev, "q")
             sp, lds = _expect(scales, (rows, max(1, self.d // qblock)), torch.float32, dev, "scales")
         else:
+            if q.dtype is torch.float8_e4m3fn:
+                raise TypeError("q holds e4m3 codes: give code='e4m3'")
             xp, ldx, qp, ldq, sp, lds = x.data_ptr(), _ld(x), q.data_ptr(), _ld(q), scales.data_ptr(), _ld(scales)
         d = HARP_FORWARD if direction == "forward" else HARP_INVERSE
         _check(lib().harp_apply_quant_ex(self._h, xp, rows, ldx, _dtype_code(x), fmt, qp, ldq, sp, lds, qblock, d,
-                                         _stream_handle(stream)), "harp_apply_quant")
+                                         _stream_handle(None)), "harp_apply_quant")
         return q, scales
 
     def grad_workspace(self, device=None):
@@ -367,6 +382,9 @@ class Plan:
         (bf16 or fp32).  qblock defaults to the one that the scales' shape gives when it divides d.
         Returns a float32 tensor of theta_count entries."""
         import torch
+        if stream is not None:
+            with _on(stream):
+                return self.grad_theta_quant(q, scales, g, dtheta, workspace, None, qblock)
         rows = q.shape[0]
         if qblock is None:
             nb = scales.shape[1] if scales.dim() == 2 else 0
@@ -390,7 +408,7 @@ class Plan:
             raise ValueError("workspace must be contiguous, on the current CUDA device")
         _check(lib().harp_grad_theta_quant(self._h, qp, ldq, code, sp, lds, qblock, gp, ldg, gt, rows, tp,
                                            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                           _stream_handle(stream)),
+                                           _stream_handle(None)),
                "harp_grad_theta_quant")
         return dtheta
 
@@ -400,6 +418,9 @@ class Plan:
         dtype on the GPU.  Returns a float32 tensor of theta_count entries (dtheta, if
         given, is filled).  dL/dx is self.apply(g, direction="inverse")."""
         import torch
+        if stream is not None:
+            with _on(stream):
+                return self.grad_theta(x, g, dtheta, workspace)
         if x.dtype != g.dtype or x.shape != g.shape or x.shape[-1] != self.d:
             raise ValueError(f"x and g must be rows of d={self.d} of one dtype")
         # a composite's schedule is its plans' schedules in a row (no theta count of its
@@ -409,12 +430,11 @@ class Plan:
             dtheta = torch.empty(n, dtype=torch.float32, device=x.device)
         if dtheta.dtype != torch.float32 or dtheta.numel() != n or not dtheta.is_contiguous():
             raise ValueError(f"dtheta must be a contiguous float32 tensor of {n} entries")
-        need = int(lib().harp_grad_workspace_bytes(self._h))
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            workspace = self.grad_workspace(x.device)
         _check(lib().harp_grad_theta(self._h, x.data_ptr(), g.data_ptr(), x.shape[0], _ld(x), _ld(g),
                                      _dtype_code(x), dtheta.data_ptr(), workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), _stream_handle(stream)),
+                                     workspace.numel() * workspace.element_size(), _stream_handle(None)),
                "harp_grad_theta")
         return dtheta
 
@@ -580,6 +600,9 @@ def quantize(x, block=(1, 128), code: str = "e4m3", q=None, scales=None, stream=
     for block = (b0, b1): (1, 32 | 64 | 128 | 256) for rows (checkpoints for Plan.grad_theta_quant;
     e4m3 with 128: matmul_quant's row operand), (128, 128) for a weight (matmul_quant's).
     Returns (q, scales).  A new q has rows a multiple of 16 bytes apart."""
+    if stream is not None:
+        with _on(stream):
+            return quantize(x, block, code, q, scales)
     _, f32, current, raw = _TORCH or _torch()
     fmt, dev = _code(code), _device(x, "x", current)
     rows, cols = shape = _rows_of(x, "x")
@@ -596,13 +619,16 @@ def quantize(x, block=(1, 128), code: str = "e4m3", q=None, scales=None, stream=
     qp, ldq = _expect(q, shape, qt, dev, "q")
     sp, lds = _expect(scales, sshape, f32, dev, "scales")
     _check(lib().harp_quantize(xp, rows, cols, ldx, dt, fmt, br, bc, qp, ldq, sp, lds,
-                               raw(dev) if stream is None else _stream_handle(stream)), "harp_quantize")
+                               raw(dev)), "harp_quantize")
     return q, scales
 
 
 def dequantize(q, scales, block=(1, 128), out=None, dtype=None, stream=None):
     """The values q * scale of quantize's codes (harp_dequantize), rounded to out's type (a new tensor
     of `dtype`, bfloat16 by default).  Returns out."""
+    if stream is not None:
+        with _on(stream):
+            return dequantize(q, scales, block, out, dtype)
     _, f32, current, raw = _TORCH or _torch()
     code, dev = _code_of(q), _device(q, "q", current)
     rows, cols = shape = _rows_of(q, "q")
@@ -619,7 +645,7 @@ def dequantize(q, scales, block=(1, 128), out=None, dtype=None, stream=None):
     dt = _dtype_code(out)
     yp, ldy = _expect(out, shape, out.dtype, dev, "out")
     _check(lib().harp_dequantize(qp, ldq, sp, lds, code, br, bc, rows, cols, yp, ldy, dt,
-                                 raw(dev) if stream is None else _stream_handle(stream)), "harp_dequantize")
+                                 raw(dev)), "harp_dequantize")
     return out
 
 
@@ -631,6 +657,9 @@ def rms_norm_quant(x, weight=None, residual=None, eps: float = 1e-6, qblock: int
     y, if given, u rounded to x's type.  Returns (q, scales, h): codes [rows, d] (int8 or
     float8_e4m3fn), float32 scales [rows, ceil(d / qblock)], and the sum (x itself without a
     residual, unless h is given)."""
+    if stream is not None:
+        with _on(stream):
+            return rms_norm_quant(x, weight, residual, eps, qblock, code, h, y, q, scales)
     _, f32, current, raw = _TORCH or _torch()
     fmt, dev = _code(code), _device(x, "x", current)
     rows, d = shape = _rows_of(x, "x")
@@ -658,7 +687,7 @@ def rms_norm_quant(x, weight=None, residual=None, eps: float = 1e-6, qblock: int
     qp, ldq = _expect(q, shape, qt, dev, "q")
     sp, lds = _expect(scales, (rows, nb), f32, dev, "scales")
     _check(lib().harp_rms_norm_quant(xp, ldx, rp, ldr, wp, rows, d, dt, eps, hp, ldh, yp, ldy, fmt, qblock, qp, ldq,
-                                     sp, lds, raw(dev) if stream is None else _stream_handle(stream)),
+                                     sp, lds, raw(dev)),
            "harp_rms_norm_quant")
     return q, scales, x if h is None else h
 
@@ -669,6 +698,9 @@ def matmul_quant(xq, xs, wq, ws, out=None, dtype=None, stream=None):
     out [rows, n] in bfloat16 (the default) or float32.  Operands 16-byte aligned with leading
     dimensions that are multiples of 16, as quantize and apply_quant make them, run on the tensor
     cores.  Returns out."""
+    if stream is not None:
+        with _on(stream):
+            return matmul_quant(xq, xs, wq, ws, out, dtype)
     f8, f32, current, raw = _TORCH or _torch()
     dev = _device(xq, "xq", current)
     rows, k = xshape = _rows_of(xq, "xq")
@@ -688,7 +720,7 @@ def matmul_quant(xq, xs, wq, ws, out=None, dtype=None, stream=None):
     dt = _dtype_code(out)
     yp, ldy = _expect(out, (rows, n), out.dtype, dev, "out")
     _check(lib().harp_matmul_quant(xp, ldx, sp, lds, wp, ldw, vp, ldv, rows, n, k, yp, ldy, dt,
-                                   raw(dev) if stream is None else _stream_handle(stream)), "harp_matmul_quant")
+                                   raw(dev)), "harp_matmul_quant")
     return out
 
 
