@@ -4,7 +4,7 @@
 // matmul_simple_kernel takes any alignment: a CTA computes 64 x 64 results, the codes of a
 // 32-wide slice of k decoded to fp32 in shared memory, each thread 4 x 4 fp32 sums per block of
 // 128, which are scaled and added up in fp32 at the block's end.
-// matmul_rows.cu holds the tensor-core kernel for few rows.
+// matmul_rows.cu holds the tensor-core kernel for few rows, matmul_tiles.cu the one for many.
 #include <algorithm>
 #include <atomic>
 #include <mutex>
@@ -117,19 +117,17 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 
 }  // namespace
 
-namespace {
-
-harp_status encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t cols, int64_t rows,
-                      int64_t pitch_bytes, int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
+harp_status matmul_tensor_map(CUtensorMap* map, const void* q, int64_t rows, int64_t k, int64_t ld, int box_rows) {
     auto encode = encoder();
     if (!encode) return harp_fail(HARP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-    const cuuint64_t dim[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t stride[1] = {(cuuint64_t)pitch_bytes};
-    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+    const cuuint64_t dim[2] = {(cuuint64_t)k, (cuuint64_t)rows};
+    const cuuint64_t stride[1] = {(cuuint64_t)ld};
+    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
     const cuuint32_t step[2] = {1, 1};
     auto run = [&] {
-        return encode(map, type, 2, const_cast<void*>(base), dim, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(q), dim, stride, box, step,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     };
     CUresult r = run();
     if (r == CUDA_ERROR_INVALID_CONTEXT) {
@@ -140,17 +138,6 @@ harp_status encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* ba
     }
     if (r != CUDA_SUCCESS) return harp_fail(HARP_ERR_CUDA, "cuTensorMapEncodeTiled failed: " + std::to_string((int)r));
     return HARP_OK;
-}
-
-}  // namespace
-
-harp_status matmul_tensor_map(CUtensorMap* map, const void* q, int64_t rows, int64_t k, int64_t ld, int box_rows) {
-    return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, k, rows, ld, 128, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
-harp_status matmul_result_map(CUtensorMap* map, void* y, int64_t rows, int64_t n, int64_t ld, bool f32) {
-    return f32 ? encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, y, n, rows, 4 * ld, 32, 128, CU_TENSOR_MAP_SWIZZLE_128B)
-               : encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, n, rows, 2 * ld, 32, 128, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 int* matmul_status_word() {

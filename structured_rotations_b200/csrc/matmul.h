@@ -1,4 +1,5 @@
-// The e4m3 product's operands and helpers, shared by its kernels (matmul.cu, matmul_rows.cu).
+// The e4m3 product's operands and helpers, shared by its kernels (matmul.cu, matmul_rows.cu,
+// matmul_tiles.cu).
 #pragma once
 
 #include <cstdint>
@@ -18,8 +19,6 @@ struct MatmulParams {
 // Map of a matrix of codes in boxes of 128 bytes x `box` rows, 128-byte swizzled; beyond the matrix the
 // boxes hold zeros (matmul.cu).
 harp_status matmul_tensor_map(CUtensorMap* map, const void* q, int64_t rows, int64_t k, int64_t ld, int box);
-// Map of the results in boxes of 32 columns x 128 rows, swizzled over the box's row length.
-harp_status matmul_result_map(CUtensorMap* map, void* y, int64_t rows, int64_t n, int64_t ld, bool f32);
 // The current device's status word of bounded waits (nullptr: no address); see harp_device_status.
 int* matmul_status_word();
 

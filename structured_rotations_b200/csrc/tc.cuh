@@ -124,20 +124,6 @@ __device__ __forceinline__ void tma_prefetch(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
-// A 4-byte copy from global to shared memory that no register waits for; copies retire in groups.
-__device__ __forceinline__ void copy4_async(const void* dst, const float* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-// The first `bytes` of 16, zeros behind them; both addresses 16-byte aligned.
-__device__ __forceinline__ void copy16_async(const void* dst, const float* src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {   // all but the last N groups have landed
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Tensor memory.  G: CTAs that share an instruction (1, or 2 for a CTA pair).
 template <int G>
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
