@@ -270,8 +270,10 @@ __device__ void stage_forward(float* A, int nr, int rs, int64_t nb, int s, const
 
 // Backward stage t: with z = z_{t+1} in A and h = h_{t+1} in H, per group and row
 //   z_t = B^T z,  dL/dB += h z_t^T,  h_t = B^T h,
-// then the tile's sums of this group go to the accumulator.
-template <int B>
+// then the tile's sums of this group go to the accumulator.  The last stage is not run forward, A still
+// holds its z_t; nothing reads the first stage's h_t and, behind it, A.
+enum Place { kMiddle, kLast, kFirst };
+template <int B, Place AT>
 __device__ void stage_backward(float* A, float* H, int nr, int rs, int64_t nb, int s, const float* lanes,
                                float* acc_t) {
     constexpr int BB = B * B;
@@ -293,16 +295,16 @@ __device__ void stage_backward(float* A, float* H, int nr, int rs, int64_t nb, i
             for (int k = 0; k < B; ++k) zo[k] = a[off[k]], ho[k] = h[off[k]];
 #pragma unroll
             for (int l = 0; l < B; ++l) {
-                float zi = 0.f, hin = 0.f;
+                float zi = AT == kLast ? zo[l] : 0.f, hin = 0.f;
 #pragma unroll
                 for (int k = 0; k < B; ++k) {
-                    zi = fmaf(w[k * B + l], zo[k], zi);
-                    hin = fmaf(w[k * B + l], ho[k], hin);
+                    if (AT != kLast) zi = fmaf(w[k * B + l], zo[k], zi);
+                    if (AT != kFirst) hin = fmaf(w[k * B + l], ho[k], hin);
                 }
 #pragma unroll
                 for (int k = 0; k < B; ++k) sum[k * B + l] = fmaf(ho[k], zi, sum[k * B + l]);
-                a[off[l]] = zi;
-                h[off[l]] = hin;
+                if (AT == kMiddle) a[off[l]] = zi;
+                if (AT != kFirst) h[off[l]] = hin;
             }
         }
         float* dst = acc_t + acc_index<BB>(c, 0, nb);
@@ -325,10 +327,12 @@ __device__ void run_stage(const GradParams& p, int t, float* A, float* H, int nr
     const int s = (int)sd.s;
     const int64_t nb = sd.nblocks;
     float* acc_t = p.acc + p.acc_off[t];
-#define HARP_GRAD_CASE(BV)                                                                 \
-    case BV:                                                                               \
-        if (FWD) stage_forward<BV>(A, nr, p.rs, nb, s, lanes);                             \
-        else stage_backward<BV>(A, H, nr, p.rs, nb, s, lanes, acc_t);                      \
+#define HARP_GRAD_CASE(BV)                                                                                     \
+    case BV:                                                                                                   \
+        if (FWD) stage_forward<BV>(A, nr, p.rs, nb, s, lanes);                                                 \
+        else if (t == 0) stage_backward<BV, kFirst>(A, H, nr, p.rs, nb, s, lanes, acc_t);                      \
+        else if (t == p.pd.m - 1) stage_backward<BV, kLast>(A, H, nr, p.rs, nb, s, lanes, acc_t);              \
+        else stage_backward<BV, kMiddle>(A, H, nr, p.rs, nb, s, lanes, acc_t);                                 \
         break;
     switch (sd.b) {
         HARP_GRAD_CASE(2)
@@ -357,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) harp_grad_blocks_kernel(const __g
         if constexpr (std::is_void<C>::value) load_tile<T>(p, A, H, row0, nr);
         else load_tile_codes<C, T>(p, A, H, row0, nr);
         __syncthreads();
-        for (int t = 0; t < m; ++t) run_stage<true>(p, t, A, H, nr);
+        for (int t = 0; t < max(1, m - 1); ++t) run_stage<true>(p, t, A, H, nr);
         for (int t = m - 1; t >= 0; --t) run_stage<false>(p, t, A, H, nr);
     }
 }
