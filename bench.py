@@ -674,12 +674,16 @@ def grad_measurement(H, W, torch, device, peak, rows=None, steps=10):
     e1.record(stream)
     torch.cuda.synchronize()
     ms = e0.elapsed_time(e1) / steps
-    fma = 4 * w.d * sum(w.schedule) * rows
+    # per coordinate: every stage's outer product, and for every stage but the last its forward and the
+    # recovery of its input, for every stage but the first the gradient's way down
+    b = w.schedule
+    per_row = w.d * (4 * sum(b) - 2 * b[-1] - b[0])
+    fma = per_row * rows
     byt = 4 * rows * w.d
     return {"workload": f"calibration backward dL/dtheta, d=4096 schedule (8,8,8,8), {rows} bf16 rows x and "
                         f"upstream gradients g (N(0,1)), theta~N(0,0.05)",
             "ms": ms, "rows_per_s": rows / (ms / 1e3), "hbm_gbs": byt / (ms / 1e3) / 1e9,
-            "hbm_frac": byt / (ms / 1e3) / 1e9 / peak, "fma_per_row": 4 * w.d * sum(w.schedule),
+            "hbm_frac": byt / (ms / 1e3) / 1e9 / peak, "fma_per_row": per_row,
             "fma_per_s": fma / (ms / 1e3),
             "kernel": "harp_grad_blocks_kernel + harp_grad_theta_kernel", "steps": steps,
             "traffic": (recorded_traffic("harp_grad_blocks_kernel", "d4096") if rows == w.rows else None)}

@@ -7,11 +7,11 @@
 //  1. harp_grad_blocks_kernel: dL/dB_{t,c} = sum_r h_{t+1,r}[group] z_{t,r}[group]^T, with
 //     z_t the input of stage t and h_{t+1} the gradient at its output.  A persistent CTA
 //     takes tiles of R rows; per tile it holds x and g in shared memory as fp32, runs the
-//     stages forward on x (z_m = y), then walks them backwards: in one pass over each
+//     stages but the last forward on x, then walks them backwards: in one pass over each
 //     group it recovers the stage's input through the transposed block (z_t = B^T z_{t+1},
-//     exact up to rounding because B is orthogonal, so no intermediate is stored), adds
-//     the outer products h (x) z over the tile's rows, and moves the gradient down
-//     (h_t = B^T h_{t+1}).  The tile's sums go to a float accumulator with one atomic
+//     exact up to rounding because B is orthogonal, so no intermediate is stored; the last
+//     stage's input is still there), adds the outer products h (x) z over the tile's rows, and
+//     moves the gradient down (h_t = B^T h_{t+1}; not below the first stage).  The tile's sums go to a float accumulator with one atomic
 //     add per element (vector atomics where the block is a multiple of 4 floats), laid out so
 //     that a warp's additions are contiguous (acc_index).
 //  2. harp_grad_theta_kernel: eight lanes per block map dL/dB to dL/dtheta in double:
@@ -20,9 +20,11 @@
 //     dL/dA[j][i] for the k-th pair i < j.
 // The device blocks of stage 0 carry the signs (B_0 diag(S)), so kernel 1 accumulates the
 // gradient of those and kernel 2 multiplies column l by the sign of its coordinate.
-// Kernel 1 has 64 FMAs per byte of bf16 rows: the FP32 pipe bounds it, at 27 % of its peak (65,536 rows of
-// d = 4096: 3.36 ms; 16,384 rows from int8 checkpoints: 0.91 ms), with 8 warps per SM because a
-// thread holds a block and its 64 sums.
+// Kernel 1 has 26 FMAs per byte of bf16 rows (four stages of radix 8): the FP32 pipe would bound it.  It
+// runs at 27 % of the pipe's peak (65,536 rows of d = 4096: 2.82 ms; 16,384 rows from int8
+// checkpoints: 0.77 ms), because a thread holds a block and its 64 sums, which leaves 8 warps per SM
+// to hide the loads of tiles and blocks, the shared-memory accesses and the atomics, each of which takes a
+// tenth to a fifth of the time.
 #include <algorithm>
 #include <type_traits>
 
@@ -52,7 +54,7 @@ struct GradParams {
     int vec;                              // rows of x and g load as 16-byte vectors
     const float* xs;                      // x as 8-bit codes: one scale per qblock coordinates of a row
     int64_t ld_xs;
-    int qblock;
+    int qshift;                           // log2 of qblock
 };
 
 // Coordinate i of a row sits at swz(i) in shared memory: bits 0-2 of i XOR bits 3-5, bits 3-4
@@ -79,6 +81,19 @@ __device__ __forceinline__ void unpack(const uint4& v, float (&f)[4]) {
     f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
 }
 
+// Item q of a tile as (row r, position j of n) for q = threadIdx.x, + kThreads, ...: one division for all of them.
+struct Walk {
+    int r, j, dr, dj, n;
+    __device__ __forceinline__ explicit Walk(int per_row) : n(per_row) {
+        r = (int)threadIdx.x / n, j = (int)threadIdx.x - r * n;
+        dr = kThreads / n, dj = kThreads - dr * n;
+    }
+    __device__ __forceinline__ void next() {
+        r += dr, j += dj;
+        if (j >= n) j -= n, ++r;
+    }
+};
+
 // x and g rows [row0, row0 + nr) into the fp32 tiles.  Each thread keeps several loads in
 // flight before it converts and stores them (a load followed directly by its store would
 // wait out the memory latency once per element).
@@ -91,22 +106,22 @@ __device__ void load_tile(const GradParams& p, float* A, float* H, int64_t row0,
         constexpr int V = 16 / sizeof(T);   // elements per 16-byte load
         constexpr int U = 4;                // vector loads of x (and of g) in flight per thread
         const int cpr = d / V, total = nr * cpr;
+        Walk from(cpr);
         for (int q0 = threadIdx.x; q0 < total; q0 += kThreads * U) {
             uint4 vx[U], vg[U];
+            Walk to = from;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int q = q0 + u * kThreads;
-                if (q < total) {
-                    const int r = q / cpr, j = q - r * cpr;
+            for (int u = 0; u < U; ++u, from.next()) {
+                const int r = from.r, j = from.j;
+                if (r < nr) {
                     vx[u] = __ldg(reinterpret_cast<const uint4*>(x + (row0 + r) * p.ld_x) + j);
                     vg[u] = __ldg(reinterpret_cast<const uint4*>(g + (row0 + r) * p.ld_g) + j);
                 }
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int q = q0 + u * kThreads;
-                if (q < total) {
-                    const int r = q / cpr, j = q - r * cpr;
+            for (int u = 0; u < U; ++u, to.next()) {
+                const int r = to.r, j = to.j;
+                if (r < nr) {
                     float fx[V], fg[V];
                     unpack(vx[u], fx);
                     unpack(vg[u], fg);
@@ -155,8 +170,9 @@ __device__ void load_tile_codes(const GradParams& p, float* A, float* H, int64_t
     const T* g = (const T*)p.g;
     constexpr int U = 4;                // groups of 8 in flight per thread
     const int cpr = (d + 7) / 8, total = nr * cpr;
-    auto put = [&](int q, const uint2& code, float s, const float (&fg)[8]) {
-        const int r = q / cpr, c = 8 * (q - r * cpr), n = min(8, d - c);
+    Walk from(cpr);
+    auto put = [&](int r, int c, const uint2& code, float s, const float (&fg)[8]) {
+        const int n = min(8, d - c);
         float lo[4], hi[4];
         C::decode4(code.x, lo);
         C::decode4(code.y, hi);
@@ -173,27 +189,26 @@ __device__ void load_tile_codes(const GradParams& p, float* A, float* H, int64_t
             uint2 code[U];
             float s[U];
             harp_codes::Eight<T> g8[U];
+            Walk to = from;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int q = q0 + u * kThreads;
-                if (q < total) {
-                    const int r = q / cpr, c = 8 * (q - r * cpr);
+            for (int u = 0; u < U; ++u, from.next()) {
+                const int r = from.r, c = 8 * from.j;
+                if (r < nr) {
                     code[u] = __ldcs(reinterpret_cast<const uint2*>(x + (row0 + r) * p.ld_x + c));
-                    s[u] = __ldg(p.xs + (row0 + r) * p.ld_xs + c / p.qblock);
+                    s[u] = __ldg(p.xs + (row0 + r) * p.ld_xs + (c >> p.qshift));
                     g8[u].load(g + (row0 + r) * p.ld_g + c);
                 }
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int q = q0 + u * kThreads;
+            for (int u = 0; u < U; ++u, to.next()) {
                 float fg[8];
                 g8[u].get(fg);
-                if (q < total) put(q, code[u], s[u], fg);
+                if (to.r < nr) put(to.r, 8 * to.j, code[u], s[u], fg);
             }
         }
     } else {
-        for (int q = threadIdx.x; q < total; q += kThreads) {
-            const int r = q / cpr, c = 8 * (q - r * cpr), n = min(8, d - c);
+        for (; from.r < nr; from.next()) {
+            const int r = from.r, c = 8 * from.j, n = min(8, d - c);
             const uint8_t* src = x + (row0 + r) * p.ld_x + c;
             uint32_t w[2] = {0u, 0u};
 #pragma unroll
@@ -201,7 +216,7 @@ __device__ void load_tile_codes(const GradParams& p, float* A, float* H, int64_t
                 if (k < n) w[k >> 2] |= (uint32_t)src[k] << (8 * (k & 3));
             float fg[8];
             harp_codes::load8(g + (row0 + r) * p.ld_g + c, n, false, fg);
-            put(q, make_uint2(w[0], w[1]), __ldg(p.xs + (row0 + r) * p.ld_xs + c / p.qblock), fg);
+            put(r, c, make_uint2(w[0], w[1]), __ldg(p.xs + (row0 + r) * p.ld_xs + (c >> p.qshift)), fg);
         }
     }
 }
@@ -242,13 +257,28 @@ __device__ __forceinline__ int64_t acc_index(int bb, int64_t c, int e, int64_t n
     return (grp * bb + e) * 32 + lane;
 }
 
+// Two fp32 values in one register pair: a b + c for both with one instruction (each rounded to nearest).
+// The backward stages take pairs of neighbouring columns (16,384 rows of d = 4096: 0.81 -> 0.77 ms; the
+// forward stage in pairs: 0.78).
+__device__ __forceinline__ uint64_t pair2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void split2(uint64_t v, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 // Forward stage t on the activation tile: z <- M_t z.
 template <int B>
-__device__ void stage_forward(float* A, int nr, int rs, int64_t nb, int s, const float* lanes) {
-    for (int64_t c = threadIdx.x; c < nb; c += kThreads) {
+__device__ void stage_forward(float* A, int nr, int rs, int nb, int s, const float* lanes) {
+    for (int c = threadIdx.x; c < nb; c += kThreads) {
         float w[B * B];
         load_block<B>(lanes, c, w);
-        const int lo = (int)(c % s), hi = (int)(c / s);
+        const int hi = (unsigned)c / (unsigned)s, lo = c - hi * s;
         int off[B];
 #pragma unroll
         for (int k = 0; k < B; ++k) off[k] = swz(lo + s * (k + B * hi));
@@ -274,37 +304,72 @@ __device__ void stage_forward(float* A, int nr, int rs, int64_t nb, int s, const
 // holds its z_t; nothing reads the first stage's h_t and, behind it, A.
 enum Place { kMiddle, kLast, kFirst };
 template <int B, Place AT>
-__device__ void stage_backward(float* A, float* H, int nr, int rs, int64_t nb, int s, const float* lanes,
+__device__ void stage_backward(float* A, float* H, int nr, int rs, int nb, int s, const float* lanes,
                                float* acc_t) {
     constexpr int BB = B * B;
-    for (int64_t c = threadIdx.x; c < nb; c += kThreads) {
+    for (int c = threadIdx.x; c < nb; c += kThreads) {
         float w[BB];
         load_block<B>(lanes, c, w);
-        const int lo = (int)(c % s), hi = (int)(c / s);
+        const int hi = (unsigned)c / (unsigned)s, lo = c - hi * s;
         int off[B];
 #pragma unroll
         for (int k = 0; k < B; ++k) off[k] = swz(lo + s * (k + B * hi));
         float sum[BB];
+        if constexpr (B % 2 == 0) {
+            uint64_t acc[BB / 2];   // pairs of neighbouring columns
 #pragma unroll
-        for (int e = 0; e < BB; ++e) sum[e] = 0.f;
-        for (int r = 0; r < nr; ++r) {
-            float* a = A + r * rs;
-            float* h = H + r * rs;
-            float zo[B], ho[B];
-#pragma unroll
-            for (int k = 0; k < B; ++k) zo[k] = a[off[k]], ho[k] = h[off[k]];
-#pragma unroll
-            for (int l = 0; l < B; ++l) {
-                float zi = AT == kLast ? zo[l] : 0.f, hin = 0.f;
+            for (int e = 0; e < BB / 2; ++e) acc[e] = 0;
+            for (int r = 0; r < nr; ++r) {
+                float* a = A + r * rs;
+                float* h = H + r * rs;
+                float zf[B];
+                uint64_t zo[B], ho[B];
 #pragma unroll
                 for (int k = 0; k < B; ++k) {
-                    if (AT != kLast) zi = fmaf(w[k * B + l], zo[k], zi);
-                    if (AT != kFirst) hin = fmaf(w[k * B + l], ho[k], hin);
+                    const float hf = h[off[k]];
+                    zf[k] = a[off[k]];
+                    zo[k] = pair2(zf[k], zf[k]), ho[k] = pair2(hf, hf);
                 }
 #pragma unroll
-                for (int k = 0; k < B; ++k) sum[k * B + l] = fmaf(ho[k], zi, sum[k * B + l]);
-                if (AT == kMiddle) a[off[l]] = zi;
-                if (AT != kFirst) h[off[l]] = hin;
+                for (int l = 0; l < B; l += 2) {
+                    uint64_t zi = 0, hin = 0;
+                    if (AT == kLast) zi = pair2(zf[l], zf[l + 1]);
+#pragma unroll
+                    for (int k = 0; k < B; ++k) {
+                        const uint64_t w2 = pair2(w[k * B + l], w[k * B + l + 1]);
+                        if (AT != kLast) zi = fma2(w2, zo[k], zi);
+                        if (AT != kFirst) hin = fma2(w2, ho[k], hin);
+                    }
+#pragma unroll
+                    for (int k = 0; k < B; ++k) acc[(k * B + l) / 2] = fma2(ho[k], zi, acc[(k * B + l) / 2]);
+                    if (AT == kMiddle) split2(zi, a[off[l]], a[off[l + 1]]);
+                    if (AT != kFirst) split2(hin, h[off[l]], h[off[l + 1]]);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < BB / 2; ++e) split2(acc[e], sum[2 * e], sum[2 * e + 1]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < BB; ++e) sum[e] = 0.f;
+            for (int r = 0; r < nr; ++r) {
+                float* a = A + r * rs;
+                float* h = H + r * rs;
+                float zo[B], ho[B];
+#pragma unroll
+                for (int k = 0; k < B; ++k) zo[k] = a[off[k]], ho[k] = h[off[k]];
+#pragma unroll
+                for (int l = 0; l < B; ++l) {
+                    float zi = AT == kLast ? zo[l] : 0.f, hin = 0.f;
+#pragma unroll
+                    for (int k = 0; k < B; ++k) {
+                        if (AT != kLast) zi = fmaf(w[k * B + l], zo[k], zi);
+                        if (AT != kFirst) hin = fmaf(w[k * B + l], ho[k], hin);
+                    }
+#pragma unroll
+                    for (int k = 0; k < B; ++k) sum[k * B + l] = fmaf(ho[k], zi, sum[k * B + l]);
+                    if (AT == kMiddle) a[off[l]] = zi;
+                    if (AT != kFirst) h[off[l]] = hin;
+                }
             }
         }
         float* dst = acc_t + acc_index<BB>(c, 0, nb);
@@ -325,7 +390,7 @@ __device__ void run_stage(const GradParams& p, int t, float* A, float* H, int nr
     const StageDesc& sd = p.pd.st[t];
     const float* lanes = p.lanes + p.lane_off[t];
     const int s = (int)sd.s;
-    const int64_t nb = sd.nblocks;
+    const int nb = (int)sd.nblocks;
     float* acc_t = p.acc + p.acc_off[t];
 #define HARP_GRAD_CASE(BV)                                                                                     \
     case BV:                                                                                                   \
@@ -629,7 +694,8 @@ harp_status grad_checked(harp_plan_t p, const void* x, const void* g, int64_t ro
         gp.rs = rs;
         gp.ntiles = (rows + R - 1) / R;
         const size_t es = dtype == HARP_F32 ? 4 : 2;
-        gp.xs = cr.scales, gp.ld_xs = cr.ld_s, gp.qblock = cr.qblock;
+        gp.xs = cr.scales, gp.ld_xs = cr.ld_s;
+        gp.qshift = cr.qblock == 32 ? 5 : cr.qblock == 64 ? 6 : cr.qblock == 128 ? 7 : 8;
         if (coded)
             gp.vec = ((uintptr_t)x % 8 == 0) && ((uintptr_t)g % 16 == 0) && ld_x % 8 == 0 && (ld_g * es) % 16 == 0;
         else
