@@ -56,35 +56,37 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantPara
     }
 }
 
-// Tiles of 128 x 128: a CTA per tile, 16 lanes across a row of the tile, 16 rows per pass.
+// Tiles of 128 x 128: a CTA per tile, 16 lanes across a row of the tile, 16 rows per pass.  HBM bounds it as long as
+// enough tiles are under way: bf16 values stay packed, four CTAs per SM instead of two (28672 x 8192: 111
+// us, 96 % of a copy, against 129; five CTAs spill: 216).  fp32 values take two CTAs' registers.
 template <typename T, typename C>
-__global__ void __launch_bounds__(kThreads) quantize_tiles_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) quantize_tiles_kernel(const QuantParams p) {
     __shared__ float part[kThreads / 32];
     const int64_t tc = (p.cols + 127) / 128;
     const int64_t tr = (int64_t)blockIdx.x / tc, tj = (int64_t)blockIdx.x % tc;
     const int64_t c = tj * 128 + 8 * (threadIdx.x & 15), r0 = tr * 128 + (threadIdx.x >> 4);
     const int n = (int)max((int64_t)0, min((int64_t)8, p.cols - c));
     const bool whole = tj * 128 + 128 <= p.cols && tr * 128 + 128 <= p.rows;   // one path without conditions
-    float v[8][8];
+    Eight<T> x[8];
     if (whole && p.vx) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            Eight<T> x;
-            x.load((const T*)p.x + (r0 + 16 * i) * p.ld_x + c);
-            x.get(v[i]);
-        }
+        for (int i = 0; i < 8; ++i) x[i].load((const T*)p.x + (r0 + 16 * i) * p.ld_x + c);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
+            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             const int64_t r = r0 + 16 * i;
-            if (n > 0 && r < p.rows) load8((const T*)p.x + r * p.ld_x + c, n, p.vx, v[i]);
+            if (n > 0 && r < p.rows) load8((const T*)p.x + r * p.ld_x + c, n, p.vx, v);
+            x[i].set(v);   // values of T: exact
         }
     }
     float a = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a = amax_nan(a, amax8(v[i]));
+    for (int i = 0; i < 8; ++i) {
+        float v[8];
+        x[i].get(v);
+        a = amax_nan(a, amax8(v));
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a = amax_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = a;
@@ -94,12 +96,18 @@ __global__ void __launch_bounds__(kThreads) quantize_tiles_kernel(const QuantPar
     const float f = code_factor<C>(a);
     if (whole && p.vq) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) store_codes8<C>(p.q + (r0 + 16 * i) * p.ld_q + c, 8, true, v[i], f);
+        for (int i = 0; i < 8; ++i) {
+            float v[8];
+            x[i].get(v);
+            store_codes8<C>(p.q + (r0 + 16 * i) * p.ld_q + c, 8, true, v, f);
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int64_t r = r0 + 16 * i;
-            if (n > 0 && r < p.rows) store_codes8<C>(p.q + r * p.ld_q + c, n, p.vq, v[i], f);
+            float v[8];
+            x[i].get(v);
+            if (n > 0 && r < p.rows) store_codes8<C>(p.q + r * p.ld_q + c, n, p.vq, v, f);
         }
     }
     if (threadIdx.x == 0) p.s[tr * p.ld_s + tj] = code_scale<C>(a);
