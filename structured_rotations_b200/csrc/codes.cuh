@@ -32,6 +32,13 @@ __device__ __forceinline__ float amax8(const float (&v)[8]) {
     return max3(max3(v[0], v[1], v[2]), max3(v[3], v[4], v[5]), max3(v[6], v[7], v[7]));
 }
 
+// Two fp32 products by one instruction, each rounded to nearest.  (Sums stay single: a pair's sum behind a
+// pair's product was made one fused operation, whose one rounding gave other int8 codes.)
+__device__ __forceinline__ void mul2(float& x, float& y, float f) {
+    asm("{ .reg .b64 a, b; mov.b64 a, {%0, %1}; mov.b64 b, {%2, %2}; mul.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a; }"
+        : "+f"(x), "+f"(y) : "f"(f));
+}
+
 // Four fp32 values as four codes in the bytes of a word, the first in the lowest byte.
 struct CodeI8 {
     static constexpr float kTop = 127.f;
@@ -159,8 +166,13 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, int n, bool vec, const 
 // Eight codes: one 8-byte store where `vec`
 template <typename C>
 __device__ __forceinline__ void store_codes8(uint8_t* p, int n, bool vec, const float (&v)[8], float factor) {
-    uint32_t lo = C::four(v[0] * factor, v[1] * factor, v[2] * factor, v[3] * factor);
-    uint32_t hi = C::four(v[4] * factor, v[5] * factor, v[6] * factor, v[7] * factor);
+    float t[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t[k] = v[k];
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) mul2(t[k], t[k + 1], factor);
+    uint32_t lo = C::four(t[0], t[1], t[2], t[3]);
+    uint32_t hi = C::four(t[4], t[5], t[6], t[7]);
     // int8 has no NaN: codes 0 in a block that is not finite (0 times its scale is NaN)
     if (!C::kNaN && factor == 0.f) lo = hi = 0u;
     if (vec && n >= 8) {
