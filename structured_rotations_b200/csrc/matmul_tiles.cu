@@ -41,7 +41,7 @@ struct Shape {
     static constexpr int kStages = NT == 256 ? 6 : 8;
     static constexpr int kBuffers = 512 / NT;
     static constexpr int kCols = kBuffers * NT;
-    static constexpr int kOutFloats = 32 * 17;   // per warp: 32 rows x 16 results, padded
+    static constexpr int kOutFloats = 32 * 33;   // per warp: 32 rows x 32 results, padded
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + 8 * kOutFloats * 4 + 256;
 };
 
@@ -232,19 +232,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (row) store_row((T*)p.y + r * p.ld_y + c0, sum, align_y >= 32);
                 continue;
             }
-            // 16 columns at a time through shared memory: two rows of 16 consecutive results per store
+            // 32 columns at a time through shared memory: a row's 32 consecutive results per store (4000 x 28001 x
+            // 4096: 476 us; two rows of 16 each: 555)
             const int64_t r0 = r - lane;
+            const int live = (int)max((int64_t)0, min((int64_t)32, p.rows - r0));
 #pragma unroll
-            for (int i = 0; i < N / 16; ++i) {
+            for (int i = 0; i < N / 32; ++i) {
                 __syncwarp();
 #pragma unroll
-                for (int c = 0; c < 16; ++c) mine[lane * 17 + c] = sum[16 * i + c];
+                for (int c = 0; c < 32; ++c) mine[lane * 33 + c] = sum[32 * i + c];
                 __syncwarp();
-                const int64_t c = c0 + 16 * i + (lane & 15);
+                const int64_t c = c0 + 32 * i + lane;
                 if (c < p.n) {
+                    T* y = (T*)p.y + r0 * p.ld_y + c;
 #pragma unroll 8
-                    for (int j = lane >> 4; j < 32; j += 2)
-                        if (r0 + j < p.rows) put((T*)p.y + (r0 + j) * p.ld_y + c, mine[j * 17 + (lane & 15)]);
+                    for (int j = 0; j < live; ++j, y += p.ld_y) put(y, mine[j * 33 + lane]);
                 }
             }
         }
