@@ -199,3 +199,18 @@ def test_capture_streams_and_threads():
     torch.cuda.synchronize()
     for o, y in zip(sets, got):
         assert torch.equal(y, _want(*o).float())
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("m,n", [(1111, 3333), (333, 4101), (1000, 2500)])
+def test_unaligned_results_of_many_rows(m, n, out):
+    """Results whose rows lie at odd distances, of 256- and 128-column tiles: exact, nothing beside them written."""
+    xq, xs, wq, ws = _exact_operands(m, n, 130, 17)
+    want = _want(xq, xs, wq, ws).float().to(out)
+    for ld in (n, n + 1, n + 7):
+        buf = torch.full((m + 2, ld), 7.0, dtype=out, device=DEV)
+        y = buf[1:m + 1, :n]
+        H.matmul_quant(xq, xs, wq, ws, out=y)
+        assert torch.equal(y, want)
+        y.fill_(7.0)
+        assert torch.all(buf == 7.0)
