@@ -259,7 +259,7 @@ HARP_API harp_status harp_dequantize(const void* q, int64_t ld_q, const float* s
  *   weight   d values of type dtype, or NULL (a weight that was folded into the next matrix).
  *   eps      1e-70 <= eps <= 1e30.
  *   h        NULL, or rows of d that receive h; may be x or residual itself (then with the same
- *            leading dimension).
+ *            leading dimension, unless there is one row).
  *   y        NULL, or rows of d that receive u rounded to dtype (the rows for harp_apply_quant_ex
  *            where the layer's input is rotated).
  *   q, scales   codes and scales as harp_quantize with 1 x qblock blocks, or both NULL.
@@ -286,7 +286,7 @@ HARP_API harp_status harp_rms_norm_quant(const void* x, int64_t ld_x, const void
  *   y        rows x n results of type out_dtype, leading dimension ld_y >= n; overlaps nothing.
  * Each sum's order depends on the sizes only, so equal calls give equal bits.  Any alignment
  * (16-byte aligned operands with leading dimensions that are multiples of 16 take the tensor
- * cores).  rows = 0 or n = 0 is a no-op; rows, n, k < 2^31.  Asynchronous on `stream`; no workspace.
+ * cores; a single row's leading dimension plays no part).  rows = 0 or n = 0 is a no-op; rows, n, k < 2^31.  Asynchronous on `stream`; no workspace.
  */
 HARP_API harp_status harp_matmul_quant(const void* x, int64_t ld_x, const float* sx, int64_t ld_sx, const void* w,
                                        int64_t ld_w, const float* sw, int64_t ld_sw, int64_t rows, int64_t n,

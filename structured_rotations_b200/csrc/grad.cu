@@ -696,11 +696,12 @@ harp_status grad_checked(harp_plan_t p, const void* x, const void* g, int64_t ro
         const size_t es = dtype == HARP_F32 ? 4 : 2;
         gp.xs = cr.scales, gp.ld_xs = cr.ld_s;
         gp.qshift = cr.qblock == 32 ? 5 : cr.qblock == 64 ? 6 : cr.qblock == 128 ? 7 : 8;
+        const bool one = rows == 1;   // a single row is never stepped past
         if (coded)
-            gp.vec = ((uintptr_t)x % 8 == 0) && ((uintptr_t)g % 16 == 0) && ld_x % 8 == 0 && (ld_g * es) % 16 == 0;
+            gp.vec = ((uintptr_t)x % 8 == 0) && ((uintptr_t)g % 16 == 0) && (one || (ld_x % 8 == 0 && (ld_g * es) % 16 == 0));
         else
-            gp.vec = ((uintptr_t)x % 16 == 0) && ((uintptr_t)g % 16 == 0) && (ld_x * es) % 16 == 0 &&
-                     (ld_g * es) % 16 == 0 && (d * es) % 16 == 0;
+            gp.vec = ((uintptr_t)x % 16 == 0) && ((uintptr_t)g % 16 == 0) &&
+                     (one || ((ld_x * es) % 16 == 0 && (ld_g * es) % 16 == 0)) && (d * es) % 16 == 0;
         const size_t smem = (size_t)R * per_row;
         const int grid = (int)std::min<int64_t>(gp.ntiles, sms_of_current_device());
         e = dtype == HARP_BF16 ? launch_blocks<__nv_bfloat16>(gp, cr, grid, smem, s)

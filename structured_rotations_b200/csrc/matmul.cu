@@ -193,6 +193,10 @@ extern "C" harp_status harp_matmul_quant(const void* x, int64_t ld_x, const floa
         ranges_overlap(y, yb, sx, ((size_t)(rows - 1) * ld_sx + kb) * 4) ||
         ranges_overlap(y, yb, sw, ((size_t)(nb - 1) * ld_sw + kb) * 4))
         return harp_fail(HARP_ERR_INVALID_ARG, "the result overlaps an operand");
+    // a single row is never stepped past: its leading dimension plays no part in the alignment
+    const int64_t whole = (k + 15) / 16 * 16;
+    if (rows == 1) ld_x = whole;
+    if (n == 1) ld_w = whole;
     const MatmulParams p{(const uint8_t*)x, (const uint8_t*)w, sx, sw, y, ld_x, ld_w, ld_sx, ld_sw, ld_y, rows, n, k, kb};
     // TMA takes 16-byte aligned operands whose rows are a multiple of 16 bytes (below 2^40) apart
     const bool tma = ((uintptr_t)x | (uintptr_t)w | (uintptr_t)ld_x | (uintptr_t)ld_w) % 16 == 0 && ld_x < (1ll << 40) &&

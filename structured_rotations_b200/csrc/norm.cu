@@ -174,7 +174,7 @@ extern "C" harp_status harp_rms_norm_quant(const void* x, int64_t ld_x, const vo
         for (int o = 0; o < 4; ++o) {
             if (!out[o].p) continue;
             for (int i = 0; i < 3; ++i) {
-                const bool in_place = o == 0 && i < 2 && out[o].p == in[i].p && out[o].ld == in[i].ld;
+                const bool in_place = o == 0 && i < 2 && out[o].p == in[i].p && (rows == 1 || out[o].ld == in[i].ld);
                 if (in[i].p && !in_place && ranges_overlap(out[o].p, out[o].n, in[i].p, in[i].n))
                     return harp_fail(HARP_ERR_INVALID_ARG, "an output overlaps an input");
             }
@@ -183,6 +183,7 @@ extern "C" harp_status harp_rms_norm_quant(const void* x, int64_t ld_x, const vo
                     return harp_fail(HARP_ERR_INVALID_ARG, "two outputs overlap");
         }
     }
+    if (rows == 1) ld_x = ld_r = ld_h = ld_y = ld_q = 0;   // a single row is never stepped past: any alignment of its end will do
     NormParams p;
     p.x = x, p.res = residual, p.w = weight;
     p.rows = rows, p.ld_x = ld_x, p.ld_r = ld_r;

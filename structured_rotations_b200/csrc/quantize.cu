@@ -201,8 +201,9 @@ QuantParams make_params(const void* v, int64_t rows, int64_t cols, int64_t ld, h
     p.ld_s = ld_s;
     p.qblock = bcols;
     p.qshift = bcols == 32 ? 5 : bcols == 64 ? 6 : bcols == 128 ? 7 : 8;
-    p.vx = (uintptr_t)v % 16 == 0 && (ld * es) % 16 == 0;
-    p.vq = (uintptr_t)q % 8 == 0 && ld_q % 8 == 0;
+    // (a single row is never stepped past: its leading dimension plays no part)
+    p.vx = (uintptr_t)v % 16 == 0 && (rows == 1 || (ld * es) % 16 == 0);
+    p.vq = (uintptr_t)q % 8 == 0 && (rows == 1 || ld_q % 8 == 0);
     return p;
 }
 

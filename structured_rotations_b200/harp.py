@@ -225,7 +225,10 @@ def _expect(t, shape, dtype, dev: int, what: str):
     if t.get_device() != dev:
         raise ValueError(f"{what} must be on the current CUDA device, not {t.device}")
     if t.is_contiguous():
-        return (t.data_ptr(), shape[1]) if len(shape) == 2 else t.data_ptr()
+        if len(shape) == 1:
+            return t.data_ptr()
+        # torch calls a single row contiguous whatever its stride, which is the leading dimension all the same
+        return t.data_ptr(), (shape[1] if shape[0] != 1 else max(t.stride(0), shape[1]))
     st = t.stride()
     if len(st) == 1:
         raise ValueError(f"{what} must be contiguous")
