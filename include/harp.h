@@ -277,7 +277,8 @@ HARP_API harp_status harp_rms_norm_quant(const void* x, int64_t ld_x, const void
  * harp_matmul_quant — the product of quantized rows and a quantized weight, y ~ x w^T:
  *   y[r][j] = sum_b sx[r][b] sw[j / 128][b] sum_{i in block b} x[r][i] w[j][i]
  * over blocks b of 128 along k (the last one may be short); e4m3 codes, products and sums in
- * fp32, the result rounded once.
+ * fp32, the result rounded once.  Where sx sw leaves fp32's normal range, the block's sum is
+ * multiplied by one scale after the other, so only a term that is itself out of range is lost.
  *   x, sx    rows x k codes (1 byte each, leading dimension ld_x >= k) and rows x ceil(k / 128)
  *            scales (ld_sx): harp_apply_quant_ex, harp_rms_norm_quant or harp_quantize with
  *            qblock 128.

@@ -64,9 +64,9 @@ __global__ void __launch_bounds__(kThreads) matmul_simple_kernel(const MatmulPar
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t r = r0 + 4 * ty + i;
-            const float s = r < p.rows ? p.sx[r * p.ld_sx + kb] * sw : 0.f;
+            const BlockFactor s = block_factor(r < p.rows ? p.sx[r * p.ld_sx + kb] : 0.f, sw);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) y[i][j] = fmaf(t[i][j], s, y[i][j]);
+            for (int j = 0; j < 4; ++j) y[i][j] = fmaf(t[i][j] * s.first, s.second, y[i][j]);
         }
     }
 #pragma unroll

@@ -36,7 +36,7 @@ struct Shape {
     static constexpr int kBuffers = BT <= 64 ? 4 : 2;   // tensor-memory buffers of BT columns
     static constexpr int kCols = kBuffers * BT < 32 ? 32 : kBuffers * BT;
     static constexpr int kPerSm = BT <= 64 ? 2 : 1;
-    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + 2 * BT * 4 + 256;
+    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + 4 * BT * 4 + 256;
 };
 
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
@@ -49,13 +49,14 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
     using S = Shape<BT>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* stages = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    float* ring = reinterpret_cast<float*>(stages + S::kStages * S::kStageBytes);   // [2][BT] scales
-    uint64_t* full = reinterpret_cast<uint64_t*>(ring + 2 * BT);
+    float* ring = reinterpret_cast<float*>(stages + S::kStages * S::kStageBytes);   // [2][2][BT] factors
+    uint64_t* full = reinterpret_cast<uint64_t*>(ring + 4 * BT);
     uint64_t* empty = full + S::kStages;
     uint64_t* tfull = empty + S::kStages;
     uint64_t* tempty = tfull + S::kBuffers;
     uint32_t* slot = reinterpret_cast<uint32_t*>(tempty + S::kBuffers);
     volatile int* failed = reinterpret_cast<volatile int*>(slot + 1);
+    int4* odd = reinterpret_cast<int4*>(slot + 4);   // [2]: for each warp of sums, whether its rows have scales to take apart
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)(blockIdx.x % split);
@@ -114,24 +115,47 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
             __syncwarp();
         }
     } else {
-        // the scale of x's row `tid` for the next block: loaded a block ahead, handed to the other
-        // threads through the ring
+        // the factor of x's row `tid` for the next block: its scales loaded a block ahead, handed to the other
+        // threads through the ring (where scales have to be taken apart, second, then first)
         const int tid = threadIdx.x;
         const bool has = tid < BT && m0 + tid < p.rows;
         const float* sx = p.sx + (has ? (m0 + tid) * p.ld_sx : 0);
         const float* sw = p.sw + tile * p.ld_sw;
-        float next = has && kb0 < kb1 ? __ldg(sx + kb0) * __ldg(sw + kb0) : 0.f;
+        float next_x = 0.f, next_w = 0.f;
+        if (has && kb0 < kb1) next_x = __ldg(sx + kb0), next_w = __ldg(sw + kb0);
         for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
-            float* sc = ring + (i & 1) * BT;
-            if (tid < BT) sc[tid] = next;
-            if (has && kb + 1 < kb1) next = __ldg(sx + kb + 1) * __ldg(sw + kb + 1);
+            float* sc = ring + (i & 1) * 2 * BT;
+            const float f = factor_or_nan(next_x, next_w);
+            const int any = __any_sync(0xffffffffu, f != f);
+            if (tid < BT) sc[tid] = f;
+            if (lane == 0) reinterpret_cast<int*>(odd + (i & 1))[warp] = any;
             asm volatile("bar.sync 1, 128;" ::: "memory");
+            const int4 o = odd[i & 1];
+            const bool apart = o.x | o.y | o.z | o.w;
+            if (has && kb + 1 < kb1) next_x = __ldg(sx + kb + 1), next_w = __ldg(sw + kb + 1);
+            if (apart) {   // hardly ever (all four warps agree, and meet again before any wait that may give up)
+                const BlockFactor g = has ? block_factor(__ldg(sx + kb), __ldg(sw + kb)) : BlockFactor{1.f, 0.f};
+                if (tid < BT) sc[tid] = g.second, sc[BT + tid] = g.first;
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+            }
             const int b = i % S::kBuffers;
             // after a wait that gave up the warps go on meeting at the barrier, without work
             if (!mbar_wait_warp(tfull + b, (i / S::kBuffers) & 1, failed, status)) continue;
             fence_after();
             const uint32_t addr = tmem + ((uint32_t)(32 * warp) << 16) + b * BT;
             constexpr int W = BT < 32 ? 16 : 32;
+            if (apart) {   // the sums meet one scale in tensor memory
+#pragma unroll 1
+                for (int c0 = 0; c0 < BT; c0 += 16) {
+                    uint32_t v[16];
+                    tmem_ld(addr + c0, v);
+                    tmem_ld_wait(v);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * sc[BT + c0 + c]);
+                    tmem_st(addr + c0, v);
+                }
+                tmem_st_wait();
+            }
 #pragma unroll
             for (int c0 = 0; c0 < BT; c0 += W) {
                 uint32_t v[W];

@@ -197,19 +197,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             float sum[N];
 #pragma unroll
             for (int c = 0; c < N; ++c) sum[c] = 0.f;
-            // scales two blocks ahead of their use
-            float x0 = row ? __ldg(sx) : 0.f, w0 = __ldg(sw), x1 = 0.f, w1 = 0.f;
-            if (kb > 1) x1 = row ? __ldg(sx + 1) : 0.f, w1 = __ldg(sw + 1);
+            // scales a block ahead of their use
+            float x1 = row ? __ldg(sx) : 0.f, w1 = __ldg(sw);
             for (int k = 0; k < kb; ++k) {
-                float x2 = 0.f, w2 = 0.f;
-                if (k + 2 < kb) x2 = row ? __ldg(sx + k + 2) : 0.f, w2 = __ldg(sw + k + 2);
+                float f = factor_or_nan(x1, w1);
+                const bool apart = __any_sync(0xffffffffu, f != f);
+                if (k + 1 < kb) x1 = row ? __ldg(sx + k + 1) : 0.f, w1 = __ldg(sw + k + 1);
                 ok = mbar_wait_warp(tfull + b, bph, failed, status);
                 if (!ok) break;
                 fence_after();
-                const float f = x0 * w0;
-                x0 = x1, w0 = w1, x1 = x2, w1 = w2;
                 const uint32_t addr = tmem + lanes + b * NT + N * half;
                 uint32_t v[2][16];
+                if (apart) {   // hardly ever: the sums meet one scale in tensor memory
+                    const BlockFactor g = block_factor(row ? __ldg(sx + k) : 0.f, __ldg(sw + k));
+#pragma unroll 1
+                    for (int c = 0; c < N; c += 16) {
+                        tmem_ld(addr + c, v[0]);
+                        tmem_ld_wait(v[0]);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[0][j] = __float_as_uint(__uint_as_float(v[0][j]) * g.first);
+                        tmem_st(addr + c, v[0]);
+                    }
+                    tmem_st_wait();
+                    f = g.second;
+                }
                 tmem_ld(addr, v[0]);
 #pragma unroll
                 for (int i = 0; i < N / 16; ++i) {
