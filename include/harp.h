@@ -241,7 +241,8 @@ HARP_API harp_status harp_quantize(const void* x, int64_t rows, int64_t cols, in
 /*
  * harp_dequantize — y = rn(code * scale) of the codes that harp_quantize (or harp_apply_quant_ex,
  * harp_rms_norm_quant) left: the checkpoint's rows back in `dtype`.  Arguments as harp_quantize,
- * with y in the place of x.
+ * with y in the place of x.  Codes of a finite scale stay finite in fp32 (the largest value's int8
+ * code would decode to one rounding above it).
  */
 HARP_API harp_status harp_dequantize(const void* q, int64_t ld_q, const float* scales, int64_t ld_s,
                                      harp_code code, int32_t brows, int32_t bcols, int64_t rows, int64_t cols,

@@ -154,6 +154,13 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const QuantParams 
             C::decode4(w[i][1], b);
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = a[k] * s[i], v[4 + k] = b[k] * s[i];
+            if constexpr (sizeof(T) == 4 && !C::kNaN) {
+                // the largest fp32 value's scale is rounded up: 127 of it is above that value again
+                if (C::kTop * s[i] > 3.40282347e38f && s[i] <= 3.40282347e38f) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] = copysignf(fminf(fabsf(v[k]), 3.40282347e38f), v[k]);
+                }
+            }
             y8[i].set(v);
         }
         store_groups<T, N>(y + at.r * p.ld_x, at.c0, 256, p.cols, p.vx, y8);
