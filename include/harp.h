@@ -286,9 +286,10 @@ HARP_API harp_status harp_rms_norm_quant(const void* x, int64_t ld_x, const void
  *   w, sw    n x k codes (ld_w >= k) and ceil(n / 128) x ceil(k / 128) scales (ld_sw):
  *            harp_quantize with 128 x 128 blocks of W (or of the rotated T_U^T W T_V).
  *   y        rows x n results of type out_dtype, leading dimension ld_y >= n; overlaps nothing.
- * Each sum's order depends on the sizes only, so equal calls give equal bits.  Any alignment
- * (16-byte aligned operands with leading dimensions that are multiples of 16 take the tensor
- * cores; a single row's leading dimension plays no part).  rows = 0 or n = 0 is a no-op; rows, n, k < 2^31.  Asynchronous on `stream`; no workspace.
+ * Each sum's order depends on the sizes and on whether the operands are aligned, so equal calls give
+ * equal bits.  Any alignment (16-byte aligned operands with leading dimensions that are multiples of
+ * 16 take the tensor cores; a single row's leading dimension plays no part).  rows = 0 or n = 0 is a
+ * no-op; rows, n, k < 2^31.  Asynchronous on `stream`; no workspace.
  */
 HARP_API harp_status harp_matmul_quant(const void* x, int64_t ld_x, const float* sx, int64_t ld_sx, const void* w,
                                        int64_t ld_w, const float* sw, int64_t ld_sw, int64_t rows, int64_t n,

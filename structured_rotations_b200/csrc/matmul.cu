@@ -207,9 +207,7 @@ extern "C" harp_status harp_matmul_quant(const void* x, int64_t ld_x, const floa
         // against 18.5), unless up to 128 rows meet so few columns that most pairs would idle while
         // the rows kernel splits k (128 x 1024 x 8192: 13.4 us against 24.5).
         const bool few = rows <= 64 || (rows <= 128 && (n + 127) / 128 <= harp_sm_count() / 8);
-        const harp_status st = few ? launch_matmul_rows(p, out_dtype, stream) : launch_matmul_tiles(p, out_dtype, stream);
-        if (st != HARP_ERR_UNSUPPORTED) return st;
-        harp_clear_error();
+        return few ? launch_matmul_rows(p, out_dtype, stream) : launch_matmul_tiles(p, out_dtype, stream);
     }
     return launch_simple(p, out_dtype, (cudaStream_t)stream);
 }

@@ -45,7 +45,7 @@ harp_status matmul_tensor_map(CUtensorMap* map, const void* q, int64_t rows, int
 // The current device's status word of bounded waits (nullptr: no address); see harp_device_status.
 int* matmul_status_word();
 
-// Few rows: 16-byte aligned operands and leading dimensions.
+// Few rows (at most 128): 16-byte aligned operands and leading dimensions.
 harp_status launch_matmul_rows(const MatmulParams& p, harp_dtype out, void* stream);
 // Many rows: the same alignment.
 harp_status launch_matmul_tiles(const MatmulParams& p, harp_dtype out, void* stream);

@@ -1,6 +1,6 @@
 // The e4m3 product for few rows (decode): tcgen05 with the weight as the M side of the tile.
 //
-// A CTA takes 128 rows of the weight (one tile of scales) and BT = 16 .. 128 rows of x, so that the
+// A CTA takes 128 rows of the weight (one tile of scales) and all rows of x, at most BT = 16 .. 128, so that the
 // weight, whose bytes bound the call, is read once and no tensor-core tile is padded to 128 rows of
 // x.  TMA brings 128-byte wide slices (one block of k) of both operands through a ring of stages;
 // one thread issues the block's four products into one of several tensor-memory buffers; the
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)(blockIdx.x % split);
     const int64_t tile = blockIdx.x / split;
-    const int64_t n0 = tile * 128, m0 = (int64_t)blockIdx.y * BT;
+    const int64_t n0 = tile * 128;
     const int kb0 = (int)(p.kb * rank / split), kb1 = (int)(p.kb * (rank + 1) / split);
 
     if (warp == 5) tmem_alloc<1>(slot, S::kCols);
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
                 unsigned char* st = stages + s * S::kStageBytes;
                 mbar_expect_tx(full + s, S::kStageBytes);
                 tma_load(st, &map_w, kb * 128, (int)n0, full + s);
-                tma_load(st + 128 * 128, &map_x, kb * 128, (int)m0, full + s);
+                tma_load(st + 128 * 128, &map_x, kb * 128, 0, full + s);
             }
             __syncwarp();
         }
@@ -118,8 +118,8 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
         // the factor of x's row `tid` for the next block: its scales loaded a block ahead, handed to the other
         // threads through the ring (where scales have to be taken apart, second, then first)
         const int tid = threadIdx.x;
-        const bool has = tid < BT && m0 + tid < p.rows;
-        const float* sx = p.sx + (has ? (m0 + tid) * p.ld_sx : 0);
+        const bool has = tid < p.rows;
+        const float* sx = p.sx + (has ? tid * p.ld_sx : 0);
         const float* sw = p.sw + tile * p.ld_sw;
         float next_x = 0.f, next_w = 0.f;
         if (has && kb0 < kb1) next_x = __ldg(sx + kb0), next_w = __ldg(sw + kb0);
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
         if (warp < 4 && j < p.n) {
 #pragma unroll
             for (int c = 0; c < BT; ++c)
-                if (m0 + c < p.rows) put(y + (m0 + c) * p.ld_y + j, sum[c]);
+                if (c < p.rows) put(y + c * p.ld_y + j, sum[c]);
         }
     } else {
         float* part = reinterpret_cast<float*>(stages);   // [BT][128]
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
         cluster_sync();
         if (warp < 4) {
             for (int c = rank; c < BT; c += split) {
-                if (m0 + c >= p.rows) break;
+                if (c >= p.rows) break;
                 const uint32_t at = smem_u32(part + c * 128 + threadIdx.x);
                 float v = 0.f;
                 for (int q = 0; q < split; ++q) {
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
                     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(t) : "r"(map_to_rank(at, q)) : "memory");
                     v += t;
                 }
-                if (j < p.n) put(y + (m0 + c) * p.ld_y + j, v);
+                if (j < p.n) put(y + c * p.ld_y + j, v);
             }
         }
         cluster_sync();   // a CTA leaves when its partial sums have been read
@@ -219,12 +219,11 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
 template <int BT, typename T>
 harp_status launch(const MatmulParams& p, cudaStream_t stream) {
     using S = Shape<BT>;
-    const int64_t tiles = (p.n + 127) / 128, mt = (p.rows + BT - 1) / BT;
+    const int64_t tiles = (p.n + 127) / 128;   // n < 2^31: at most 2^24, times at most 8
     // split k until the CTAs fill the SMs' slots (or a share would be under two blocks)
     const int64_t slots = (int64_t)S::kPerSm * harp_sm_count();
     int split = 1;
-    while (split < 8 && tiles * mt * split * 2 <= slots && p.kb >= 4 * split) split *= 2;
-    if (tiles * split > 0x7fffffffll || mt > 65535) return HARP_ERR_UNSUPPORTED;
+    while (split < 8 && tiles * split * 2 <= slots && p.kb >= 4 * split) split *= 2;
     CUtensorMap mx, mw;
     harp_status st;
     if ((st = matmul_tensor_map(&mx, p.x, p.rows, p.k, p.ld_x, BT)) != HARP_OK) return st;
@@ -235,7 +234,7 @@ harp_status launch(const MatmulParams& p, cudaStream_t stream) {
     cudaError_t e = (cudaError_t)harp_set_smem_limit((const void*)kern, (int)S::kSmem);
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(tiles * split), (unsigned)mt);
+        cfg.gridDim = dim3((unsigned)(tiles * split));
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = S::kSmem;
         cfg.stream = stream;
