@@ -498,7 +498,9 @@ HARP_API harp_status harp_plan_device_status(harp_plan_t plan);
 
 /* harp_device_status — the same for the entry points without a plan (harp_matmul_quant) on
  * the current device: synchronizes it and returns HARP_ERR_TIMEOUT if a bounded wait gave up since
- * the last call (the result of that call is then not valid). */
+ * the last call of harp_device_status (results computed since then are not valid).  There is one
+ * word per device, which all host threads and streams share: the call that reports a timeout clears
+ * it, whoever launched the kernel, so one thread should ask for all. */
 HARP_API harp_status harp_device_status(void);
 
 /* harp_plan_destroy — free the plan and its device memory (synchronizes the
@@ -523,9 +525,11 @@ HARP_API const char* harp_last_error(void);
  * copies and polls them only `poll_limit` times, so the first wait of each staged tile runs
  * out: the kernel then sets the plan's status word (harp_plan_device_status reports
  * HARP_ERR_TIMEOUT), retires the extra bytes itself, waits (bounded as usual) for the copies
- * it really issued, and finishes with correct output.  No copy is left in flight and no
- * wait is unbounded.  poll_limit >= 1 and 1 <= extra_bytes <= 4096, or both 0 to clear;
- * else HARP_ERR_INVALID_ARG.
+ * it really issued, and finishes with correct output.  Launches of harp_matmul_quant's tensor-core
+ * kernels expect the bytes too and give up after `poll_limit` clocks: they set the device's status
+ * word (harp_device_status reports HARP_ERR_TIMEOUT), wait for their copies, free their tensor
+ * memory and leave y undefined.  No copy is left in flight and no wait is unbounded.
+ * poll_limit >= 1 and 1 <= extra_bytes <= 4096, or both 0 to clear; else HARP_ERR_INVALID_ARG.
  */
 HARP_API harp_status harp_test_inject_wait_timeout(int64_t poll_limit, uint32_t extra_bytes);
 

@@ -71,6 +71,8 @@ extern "C" harp_status harp_test_inject_wait_timeout(int64_t poll_limit, uint32_
     return HARP_OK;
 }
 
+WaitInjection harp_wait_injection() { return {g_inject_limit, g_inject_extra}; }
+
 harp_status launch_apply_tiled(const harp_plan_s* p, const void* x, void* y, int64_t rows, int64_t ld_x,
                                int64_t ld_y, harp_dtype in_dtype, harp_dtype out_dtype, harp_dir dir,
                                void* stream, const QuantOut* quant) {

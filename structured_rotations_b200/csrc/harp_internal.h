@@ -79,6 +79,12 @@ void harp_set_last_kernel(const char* name);
 int harp_set_smem_limit(const void* kernel, int bytes);
 // SMs of the current device (api.cu)
 int harp_sm_count();
+// What harp_test_inject_wait_timeout asked for on this host thread ({0, 0}: nothing; apply_tiled.cu)
+struct WaitInjection {
+    int64_t limit;
+    uint32_t extra_bytes;
+};
+WaitInjection harp_wait_injection();
 
 // device helpers (materialize.cu)
 harp_status harp_device_free(harp_plan_s* p);

@@ -160,6 +160,11 @@ int* matmul_status_word() {
     return p;
 }
 
+harp_tc::WaitLimit matmul_wait_limit() {
+    const WaitInjection w = harp_wait_injection();
+    return {w.extra_bytes ? (long long)w.limit : harp_tc::kWaitClocks, w.extra_bytes};
+}
+
 extern "C" harp_status harp_device_status(void) {
     harp_clear_error();
     int* word = matmul_status_word();

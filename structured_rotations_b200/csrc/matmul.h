@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "harp.h"
+#include "tc.cuh"
 
 struct MatmulParams {
     const uint8_t *x, *w;        // codes: rows x k, n x k
@@ -44,6 +45,8 @@ __device__ __forceinline__ BlockFactor block_factor(float sx, float sw) {
 harp_status matmul_tensor_map(CUtensorMap* map, const void* q, int64_t rows, int64_t k, int64_t ld, int box);
 // The current device's status word of bounded waits (nullptr: no address); see harp_device_status.
 int* matmul_status_word();
+// The limit of this host thread's next launches (tc.cuh; harp_test_inject_wait_timeout).
+harp_tc::WaitLimit matmul_wait_limit();
 
 // Few rows (at most 128): 16-byte aligned operands and leading dimensions.
 harp_status launch_matmul_rows(const MatmulParams& p, harp_dtype out, void* stream);

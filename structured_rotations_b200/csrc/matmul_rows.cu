@@ -45,7 +45,8 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bf
 template <int BT, typename T>
 __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
     matmul_rows_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-                       const __grid_constant__ MatmulParams p, int split, int* status) {
+                       const __grid_constant__ MatmulParams p, int split, int* status,
+                       const __grid_constant__ WaitLimit limit) {
     using S = Shape<BT>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* stages = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -89,10 +90,10 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
     if (warp == 4) {
         for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
             const int s = i % S::kStages;
-            if (i >= S::kStages && !mbar_wait_warp(empty + s, ((i / S::kStages) & 1) ^ 1, failed, status)) break;
+            if (i >= S::kStages && !mbar_wait_warp(empty + s, ((i / S::kStages) & 1) ^ 1, failed, status, limit)) break;
             if (elect_one()) {
                 unsigned char* st = stages + s * S::kStageBytes;
-                mbar_expect_tx(full + s, S::kStageBytes);
+                mbar_expect_tx(full + s, S::kStageBytes + limit.extra_tx);
                 tma_load(st, &map_w, kb * 128, (int)n0, full + s);
                 tma_load(st + 128 * 128, &map_x, kb * 128, 0, full + s);
             }
@@ -101,8 +102,8 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
     } else if (warp == 5) {
         for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
             const int s = i % S::kStages, b = i % S::kBuffers;
-            if (!mbar_wait_warp(full + s, (i / S::kStages) & 1, failed, status)) break;
-            if (i >= S::kBuffers && !mbar_wait_warp(tempty + b, ((i / S::kBuffers) & 1) ^ 1, failed, status)) break;
+            if (!mbar_wait_warp(full + s, (i / S::kStages) & 1, failed, status, limit)) break;
+            if (i >= S::kBuffers && !mbar_wait_warp(tempty + b, ((i / S::kBuffers) & 1) ^ 1, failed, status, limit)) break;
             fence_after();
             const uint64_t a = operand_desc(stages + s * S::kStageBytes);
             const uint64_t bd = operand_desc(stages + s * S::kStageBytes + 128 * 128);
@@ -121,6 +122,7 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
         const bool has = tid < p.rows;
         const float* sx = p.sx + (has ? tid * p.ld_sx : 0);
         const float* sw = p.sw + tile * p.ld_sw;
+        bool dead = false;
         float next_x = 0.f, next_w = 0.f;
         if (has && kb0 < kb1) next_x = __ldg(sx + kb0), next_w = __ldg(sw + kb0);
         for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
@@ -139,8 +141,8 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
                 asm volatile("bar.sync 1, 128;" ::: "memory");
             }
             const int b = i % S::kBuffers;
-            // after a wait that gave up the warps go on meeting at the barrier, without work
-            if (!mbar_wait_warp(tfull + b, (i / S::kBuffers) & 1, failed, status)) continue;
+            // after a wait that gave up the warps go on meeting at the barrier, without work or further waits
+            if (dead || (dead = !mbar_wait_warp(tfull + b, (i / S::kBuffers) & 1, failed, status, limit))) continue;
             fence_after();
             const uint32_t addr = tmem + ((uint32_t)(32 * warp) << 16) + b * BT;
             constexpr int W = BT < 32 ? 16 : 32;
@@ -247,7 +249,7 @@ harp_status launch(const MatmulParams& p, cudaStream_t stream) {
         attr[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 2;
-        e = cudaLaunchKernelEx(&cfg, kern, mx, mw, p, split, status);
+        e = cudaLaunchKernelEx(&cfg, kern, mx, mw, p, split, status, matmul_wait_limit());
         if (e == cudaSuccess) e = cudaGetLastError();
     }
     if (e != cudaSuccess) {

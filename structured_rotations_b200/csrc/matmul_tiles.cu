@@ -97,7 +97,8 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* y, const float (&v)[N],
 template <int NT, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     matmul_tiles_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-                        const __grid_constant__ MatmulParams p, int64_t mt, int64_t nt, int align_y, int* status) {
+                        const __grid_constant__ MatmulParams p, int64_t mt, int64_t nt, int align_y, int* status,
+                        const __grid_constant__ WaitLimit limit) {
     using S = Shape<NT>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* stages = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -137,11 +138,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const TileOf at = tile_of(t, mt, nt);
             const int m0 = (int)(at.m * 256 + 128 * rank), n0 = (int)(at.n * NT + NT / 2 * rank);
             for (int k = 0; k < kb; ++k) {
-                if (used >= S::kStages && !(ok = mbar_wait_warp(empty + s, ph ^ 1, failed, status))) break;
+                if (used >= S::kStages && !(ok = mbar_wait_warp(empty + s, ph ^ 1, failed, status, limit))) break;
                 if (elect_one()) {
                     unsigned char* st = stages + s * S::kStageBytes;
                     const uint32_t bar = map_to_rank(smem_u32(full + s), 0);
-                    if (rank == 0) mbar_expect_tx(full + s, 2 * S::kStageBytes);
+                    if (rank == 0) mbar_expect_tx(full + s, 2 * S::kStageBytes + limit.extra_tx);
                     tma_load_pair(st, &map_x, k * 128, m0, bar);
                     tma_load_pair(st + S::kA, &map_w, k * 128, n0, bar);
                 }
@@ -152,8 +153,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         // the pair's last products have released every stage: no arrival on this CTA's barriers is left
         for (int i = 0; ok && i < S::kStages; ++i) {
-            if (used >= S::kStages) ok = mbar_wait_warp(empty + s, ph ^ 1, failed, status);
-            else if (i < used) ok = mbar_wait_warp(empty + i, 0, failed, status);
+            if (used >= S::kStages) ok = mbar_wait_warp(empty + s, ph ^ 1, failed, status, limit);
+            else if (i < used) ok = mbar_wait_warp(empty + i, 0, failed, status, limit);
             if (++s == S::kStages) s = 0, ph ^= 1;
         }
     } else if (warp == 9) {
@@ -162,8 +163,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool ok = true, ready = false;   // ready: the next stage was seen full while the last products were issued
         for (int64_t t = pair; ok && rank == 0 && t < tiles; t += pairs) {
             for (int k = 0; k < kb; ++k) {
-                if (!ready && !(ok = mbar_wait_warp(full + s, ph, failed, status))) break;
-                if (used >= S::kBuffers && !(ok = mbar_wait_warp(tempty + b, bph ^ 1, failed, status))) break;
+                if (!ready && !(ok = mbar_wait_warp(full + s, ph, failed, status, limit))) break;
+                if (used >= S::kBuffers && !(ok = mbar_wait_warp(tempty + b, bph ^ 1, failed, status, limit))) break;
                 fence_after();
                 if (elect_one()) {
                     const uint64_t a = operand_desc(stages + s * S::kStageBytes);
@@ -203,7 +204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 float f = factor_or_nan(x1, w1);
                 const bool apart = __any_sync(0xffffffffu, f != f);
                 if (k + 1 < kb) x1 = row ? __ldg(sx + k + 1) : 0.f, w1 = __ldg(sw + k + 1);
-                ok = mbar_wait_warp(tfull + b, bph, failed, status);
+                ok = mbar_wait_warp(tfull + b, bph, failed, status, limit);
                 if (!ok) break;
                 fence_after();
                 const uint32_t addr = tmem + lanes + b * NT + N * half;
@@ -287,7 +288,7 @@ harp_status launch(const MatmulParams& p, cudaStream_t stream) {
     cudaError_t e = (cudaError_t)harp_set_smem_limit((const void*)kern, (int)S::kSmem);
     if (e == cudaSuccess) {
         const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(mt * nt, harp_sm_count() / 2));
-        kern<<<(unsigned)(2 * pairs), kThreads, S::kSmem, stream>>>(mx, mw, p, mt, nt, align_y, status);
+        kern<<<(unsigned)(2 * pairs), kThreads, S::kSmem, stream>>>(mx, mw, p, mt, nt, align_y, status, matmul_wait_limit());
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) {

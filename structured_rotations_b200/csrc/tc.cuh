@@ -8,7 +8,13 @@
 
 namespace harp_tc {
 
-constexpr long long kWaitClocks = 4000000000ll;   // about two seconds: then a wait gives up
+// When a wait gives up, and bytes that a load's barrier expects beyond those that are copied (0 but for the
+// test hook of the waits that run out).
+struct WaitLimit {
+    long long clocks;
+    uint32_t extra_tx;
+};
+constexpr long long kWaitClocks = 4000000000ll;   // about two seconds
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -54,7 +60,7 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
 
 // Bounded wait for the phase of `parity`.  A wait that gives up sets *failed (this CTA's flag in
 // shared memory, which ends the CTA's other waits too) and the device's status word.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* failed, int* status) {
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* failed, int* status, const WaitLimit& limit) {
     const uint32_t addr = smem_u32(bar);
     long long t0 = 0;
     for (int i = 0;; ++i) {
@@ -69,7 +75,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
         if ((i & 63) == 63) {
             if (*failed) return false;
             if (i == 63) t0 = clock64();
-            else if (clock64() - t0 > kWaitClocks) break;
+            else if (clock64() - t0 > limit.clocks) break;
         }
         if (i == 1 << 30) break;
     }
@@ -79,8 +85,9 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 }
 
 // The same for a converged warp, with one answer for all lanes.
-__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* failed, int* status) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, failed, status));
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* failed, int* status,
+                                               const WaitLimit& limit) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, failed, status, limit));
 }
 
 // Whether the phase is over now (false says nothing), the same answer for all lanes of a converged warp.

@@ -577,7 +577,8 @@ def l_diag(w, h, qblock: int, out=None, stream=None):
 
 def inject_wait_timeout(poll_limit: int = 0, extra_bytes: int = 0) -> None:
     """Test hook (harp_test_inject_wait_timeout): make the staging waits of this thread's
-    next tiled-kernel launches run out after poll_limit polls; (0, 0) clears it."""
+    next tiled-kernel launches run out after poll_limit polls, and the waits of its matmul_quant
+    launches on the tensor cores after poll_limit clocks; (0, 0) clears it."""
     _check(lib().harp_test_inject_wait_timeout(poll_limit, extra_bytes), "harp_test_inject_wait_timeout")
 
 
@@ -729,5 +730,6 @@ def matmul_quant(xq, xs, wq, ws, out=None, dtype=None, stream=None):
 
 def device_status() -> None:
     """Synchronize the current device and raise HarpError(HARP_ERR_TIMEOUT) if a bounded device wait of
-    matmul_quant gave up since the last call (harp_device_status)."""
+    matmul_quant gave up since the last call (harp_device_status).  The device has one status word for all
+    threads and streams: the call that raises clears it, whoever launched the kernel."""
     _check(lib().harp_device_status(), "harp_device_status")
