@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
     uint64_t* tempty = tfull + S::kBuffers;
     uint32_t* slot = reinterpret_cast<uint32_t*>(tempty + S::kBuffers);
     volatile int* failed = reinterpret_cast<volatile int*>(slot + 1);
-    int4* odd = reinterpret_cast<int4*>(slot + 4);   // [2]: for each warp of sums, whether its rows have scales to take apart
+    volatile int* odd = reinterpret_cast<volatile int*>(slot + 2);   // [2]: 1 + the last block whose scales are to be taken apart
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)(blockIdx.x % split);
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
         tma_prefetch(&map_w);
         for (int i = 0; i < S::kStages; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1);
         for (int i = 0; i < S::kBuffers; ++i) mbar_init(tfull + i, 1), mbar_init(tempty + i, 4);
-        *failed = 0;
+        *failed = odd[0] = odd[1] = 0;
         mbar_init_fence();
     }
     fence_before();
@@ -122,7 +122,6 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
         const bool has = tid < p.rows;
         const float* sx = p.sx + (has ? tid * p.ld_sx : 0);
         const float* sw = p.sw + tile * p.ld_sw;
-        bool dead = false;
         float next_x = 0.f, next_w = 0.f;
         if (has && kb0 < kb1) next_x = __ldg(sx + kb0), next_w = __ldg(sw + kb0);
         for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
@@ -130,10 +129,9 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
             const float f = factor_or_nan(next_x, next_w);
             const int any = __any_sync(0xffffffffu, f != f);
             if (tid < BT) sc[tid] = f;
-            if (lane == 0) reinterpret_cast<int*>(odd + (i & 1))[warp] = any;
+            if (any && lane == 0) odd[i & 1] = kb + 1;
             asm volatile("bar.sync 1, 128;" ::: "memory");
-            const int4 o = odd[i & 1];
-            const bool apart = o.x | o.y | o.z | o.w;
+            const bool apart = odd[i & 1] == kb + 1;
             if (has && kb + 1 < kb1) next_x = __ldg(sx + kb + 1), next_w = __ldg(sw + kb + 1);
             if (apart) {   // hardly ever (all four warps agree, and meet again before any wait that may give up)
                 const BlockFactor g = has ? block_factor(__ldg(sx + kb), __ldg(sw + kb)) : BlockFactor{1.f, 0.f};
@@ -141,8 +139,14 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
                 asm volatile("bar.sync 1, 128;" ::: "memory");
             }
             const int b = i % S::kBuffers;
-            // after a wait that gave up the warps go on meeting at the barrier, without work or further waits
-            if (dead || (dead = !mbar_wait_warp(tfull + b, (i / S::kBuffers) & 1, failed, status, limit))) continue;
+            if (!mbar_wait_warp(tfull + b, (i / S::kBuffers) & 1, failed, status, limit)) {
+                // it gave up: the warp goes on meeting the others at their barriers, no more
+                for (int q = kb + 1; q < kb1; ++q) {
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    if (odd[(q - kb0) & 1] == q + 1) asm volatile("bar.sync 1, 128;" ::: "memory");
+                }
+                break;
+            }
             fence_after();
             const uint32_t addr = tmem + ((uint32_t)(32 * warp) << 16) + b * BT;
             constexpr int W = BT < 32 ? 16 : 32;
