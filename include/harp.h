@@ -210,6 +210,11 @@ HARP_API harp_status harp_apply_quant(harp_plan_t plan, const void* x, int64_t r
  * harp_quantize (Q = 448; a row that holds a NaN or an infinity keeps it in its scales): the row
  * operand of harp_matmul_quant when qblock = 128.  Kernels, alignment and errors as
  * harp_apply_quant; harp_apply_quant takes no NaN into its scales.
+ * The kernels differ in the last bits: the specialized d = 4096 kernel's three TF32 products err
+ * by 2e-7 of a block's maximum (root mean square; 1.5e-6 with HARP_CODE_I8, whose hi parts are
+ * truncated), fp32 products by 1e-7, so the same row may get other codes, about one in 10^5 (one in
+ * 40,000), in a batch below 32 rows or on another kernel.  HARP_KERNEL=tiled in the environment
+ * keeps every batch on fp32 products (1.3 times the time at d = 4096, forward).
  */
 HARP_API harp_status harp_apply_quant_ex(harp_plan_t plan, const void* x, int64_t rows, int64_t ld_x,
                                          harp_dtype in_dtype, harp_code code, void* q, int64_t ld_q,

@@ -344,7 +344,9 @@ class Plan:
         """T x (or T^T x) with the fused blockwise quantizer (harp_apply_quant_ex): bf16 rows in,
         codes [rows, d] (int8, or float8_e4m3fn for code="e4m3") and float32 scales
         [rows, d / qblock] out, y ~= q * scale per aligned block of qblock coordinates.
-        Returns (q, scales); e4m3 codes in blocks of 128 are matmul_quant's row operand."""
+        Returns (q, scales); e4m3 codes in blocks of 128 are matmul_quant's row operand.  Forward batches of
+        32 rows or more of a d = 4096 (8,8,8,8) plan are multiplied in TF32 hi and lo parts, all others in
+        fp32 (see harp_apply_quant_ex for how far the codes differ)."""
         import torch
         if stream is not None:
             with _on(stream):
