@@ -197,7 +197,8 @@ HARP_API harp_status harp_apply_host(harp_plan_t plan, const void* x, void* y, i
  *   qblock   32, 64, 128 or 256, dividing d; else HARP_ERR_INVALID_ARG.
  * x, q and scales must not overlap.  Runs on the specialized d = 4096 (8,8,8,8) kernel for
  * that schedule, forward, from 32 rows up, else on the general tiled kernel: radices <= 8,
- * d % 8 == 0, x and q rows 16-byte aligned (ld_q a multiple of 16), scales 4-byte aligned;
+ * d % 8 == 0, x and q rows 16-byte aligned (ld_q a multiple of 16 unless there is one row), scales
+ * 4-byte aligned;
  * otherwise HARP_ERR_UNSUPPORTED.  rows = 0 is a no-op.  Asynchronous on `stream`.
  */
 HARP_API harp_status harp_apply_quant(harp_plan_t plan, const void* x, int64_t rows, int64_t ld_x,
@@ -212,9 +213,9 @@ HARP_API harp_status harp_apply_quant(harp_plan_t plan, const void* x, int64_t r
  * harp_apply_quant; harp_apply_quant takes no NaN into its scales.
  * The kernels differ in the last bits: the specialized d = 4096 kernel's three TF32 products err
  * by 2e-7 of a block's maximum (root mean square; 1.5e-6 with HARP_CODE_I8, whose hi parts are
- * truncated), fp32 products by 1e-7, so the same row may get other codes, about one in 10^5 (one in
- * 40,000), in a batch below 32 rows or on another kernel.  HARP_KERNEL=tiled in the environment
- * keeps every batch on fp32 products (1.3 times the time at d = 4096, forward).
+ * truncated), fp32 products by 1e-7, so a row may get other codes (about one e4m3 code in 10^5) in a
+ * batch below 32 rows, which another kernel takes.  HARP_KERNEL=tiled in the environment keeps
+ * every batch on fp32 products (1.3 times the time at d = 4096, forward).
  */
 HARP_API harp_status harp_apply_quant_ex(harp_plan_t plan, const void* x, int64_t rows, int64_t ld_x,
                                          harp_dtype in_dtype, harp_code code, void* q, int64_t ld_q,

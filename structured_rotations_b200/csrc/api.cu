@@ -183,6 +183,7 @@ extern "C" harp_status harp_apply_quant_ex(harp_plan_t p, const void* x, int64_t
                  sb = ((rows - 1) * ld_s + d / qblock) * sizeof(float);
     if (ranges_overlap(x, xb, q, qb) || ranges_overlap(x, xb, scales, sb) || ranges_overlap(q, qb, scales, sb))
         return harp_fail(HARP_ERR_INVALID_ARG, "x, q and scales overlap");
+    if (rows == 1) ld_x = ld_q = d;   // a single row is never stepped past (d is a multiple of 32 here)
     const int choice = kernel_choice();
     if (choice == kAuto || choice == kFast) {
         st = launch_apply_fast_quant(p, x, rows, ld_x, q, ld_q, scales, ld_s, qblock, code, dir, stream);

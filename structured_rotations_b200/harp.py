@@ -224,11 +224,8 @@ def _expect(t, shape, dtype, dev: int, what: str):
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{what} must be on the current CUDA device, not {t.device}")
-    if t.is_contiguous():
-        if len(shape) == 1:
-            return t.data_ptr()
-        # torch calls a single row contiguous whatever its stride, which is the leading dimension all the same
-        return t.data_ptr(), (shape[1] if shape[0] != 1 else max(t.stride(0), shape[1]))
+    if t.is_contiguous():   # also a single row of any stride, whose leading dimension no entry looks at
+        return (t.data_ptr(), shape[1]) if len(shape) == 2 else t.data_ptr()
     st = t.stride()
     if len(st) == 1:
         raise ValueError(f"{what} must be contiguous")

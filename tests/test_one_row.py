@@ -12,15 +12,12 @@ from structured_rotations_b200 import harp as HB
 DEV = "cuda"
 
 
-def test_a_single_row_keeps_its_stride():
-    """The binding's leading dimension of the views that quantize and rms_norm_quant return."""
-    for rows in (1, 2, 5):
-        v = torch.empty(rows, 176)[:, :162]
-        assert HB._expect(v, (rows, 162), torch.float32, -1, "v")[1] == 176
-    assert HB._expect(torch.empty(1, 162), (1, 162), torch.float32, -1, "v")[1] == 162
-    assert HB._expect(torch.empty(0, 162), (0, 162), torch.float32, -1, "v")[1] == 162
-    # a stride below the width, which a single row may have, is raised to it
-    assert HB._expect(torch.empty(162, 1).t(), (1, 162), torch.float32, -1, "v")[1] == 162
+def test_a_single_row_of_any_stride_is_taken():
+    """torch calls every view of one row contiguous; its stride may be anything, and the binding's leading
+    dimension is at least the width."""
+    for v in (torch.empty(1, 176)[:, :162], torch.empty(1, 162), torch.empty(162, 1).t(), torch.empty(400).as_strided((1, 162), (7, 1))):
+        assert HB._expect(v, (1, 162), torch.float32, -1, "v")[1] >= 162
+    assert HB._expect(torch.empty(2, 176)[:, :162], (2, 162), torch.float32, -1, "v")[1] == 176
 
 
 def _exact(m, n, k, seed):
@@ -129,3 +126,18 @@ def test_gradient_of_one_row(code):
     assert torch.equal(odd, want)
     f = plan.grad_theta(x, g)
     assert torch.equal(plan.grad_theta(x.as_strided((1, 512), (513, 1)), g.as_strided((1, 512), (513, 1))), f)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("direction", ["forward", "inverse"])
+def test_rotation_of_one_row_with_any_stride(code, direction):
+    """Codes and bf16 rows whose leading dimensions no vector access divides: the same codes, nothing beside them."""
+    plan = H.Plan(1024, (8, 8, 8, 2), sign_seed=3).materialize()
+    x = torch.randn(1, 1024, device=DEV).bfloat16()
+    want, ws = plan.apply_quant(x, 64, direction, code=code)
+    buf = torch.full((1, 1031), 3, dtype=torch.uint8, device=DEV)
+    q = buf[:, :1024].view(want.dtype)
+    _, s = plan.apply_quant(x.as_strided((1, 1024), (1027, 1)), 64, direction, q=q, code=code)
+    assert torch.equal(q.view(torch.uint8), want.view(torch.uint8)) and torch.equal(s, ws)
+    assert torch.all(buf[:, 1024:] == 3)
