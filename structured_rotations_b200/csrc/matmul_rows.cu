@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
         const float* sx = p.sx + (has ? tid * p.ld_sx : 0);
         const float* sw = p.sw + tile * p.ld_sw;
         float next_x = 0.f, next_w = 0.f;
-        if (has && kb0 < kb1) next_x = __ldg(sx + kb0), next_w = __ldg(sw + kb0);
+        if (has && kb0 < kb1) next_x = load_after_wait(sx + kb0), next_w = load_after_wait(sw + kb0);
         for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
             float* sc = ring + (i & 1) * 2 * BT;
             const float f = factor_or_nan(next_x, next_w);
@@ -132,9 +132,9 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::kPerSm)
             if (any && lane == 0) odd[i & 1] = kb + 1;
             asm volatile("bar.sync 1, 128;" ::: "memory");
             const bool apart = odd[i & 1] == kb + 1;
-            if (has && kb + 1 < kb1) next_x = __ldg(sx + kb + 1), next_w = __ldg(sw + kb + 1);
+            if (has && kb + 1 < kb1) next_x = load_after_wait(sx + kb + 1), next_w = load_after_wait(sw + kb + 1);
             if (apart) {   // hardly ever (all four warps agree, and meet again before any wait that may give up)
-                const BlockFactor g = has ? block_factor(__ldg(sx + kb), __ldg(sw + kb)) : BlockFactor{1.f, 0.f};
+                const BlockFactor g = has ? block_factor(load_after_wait(sx + kb), load_after_wait(sw + kb)) : BlockFactor{1.f, 0.f};
                 if (tid < BT) sc[tid] = g.second, sc[BT + tid] = g.first;
                 asm volatile("bar.sync 1, 128;" ::: "memory");
             }
