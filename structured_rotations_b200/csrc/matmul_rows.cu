@@ -8,9 +8,9 @@
 // fp32 registers while the next blocks' products run.  With few weight tiles a cluster of C CTAs
 // splits k: each keeps the sums of its share, and they are added over distributed shared memory in
 // the order of the ranks, so that equal calls give equal bits.
-// Measured: 1 x 28672 x 8192 in 41 us, 5.7 TB/s of the weight's bytes (a copy: 6.5); 24 x 5120 x 5120 in 9.3
-// us, where the launch, the first loads and the sum over the cluster count; all scales of a CTA loaded
-// at its start instead of a block ahead: no faster.
+// Measured: 1 x 28672 x 8192 in 41 us, 5.7 TB/s of the weight's bytes (a copy: 6.5); 64 rows in 42; 24 x 5120 x
+// 5120 in 9.7, where the launch, the first loads and the sum over the cluster count; all scales of a CTA
+// loaded at its start instead of a block ahead: no faster.
 //   warps 0-3  sums: thread = one weight row (a lane of tensor memory), BT registers
 //   warp 4     TMA loads;  warp 5  tensor-memory allocation and tcgen05.mma
 #include <algorithm>

@@ -58,7 +58,8 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantPara
 
 // Tiles of 128 x 128: a CTA per tile, 16 lanes across a row of the tile, 16 rows per pass.  HBM bounds it as long as
 // enough tiles are under way: bf16 values stay packed, four CTAs per SM instead of two (28672 x 8192: 111
-// us, 96 % of a copy, against 129; five CTAs spill: 216).  fp32 values take two CTAs' registers.
+// us, 96 % of a copy, against 129, although 64 registers spill some 60 bytes; five CTAs spill more: 216).  fp32
+// values take two CTAs' registers (28672 x 8192: 173 us, 6.8 TB/s).
 template <typename T, typename C>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) quantize_tiles_kernel(const QuantParams p) {
     __shared__ float part[kThreads / 32];
