@@ -11,15 +11,14 @@
 //   warp 8     TMA loads of this CTA's operands, completing on the leader's barrier
 //   warp 9     tensor-memory allocation; in the leader (rank 0) tcgen05.mma for both CTAs
 //
-// Measured on 4096 x 28672 x 8192 (25 rounds of 64 blocks on 74 pairs): 0.90 ms in a burst (2.1 PFLOP/s), 1.05 ms under
-// the power cap, at a median of 1.54 GHz: 1,010 clocks a block, of which the tensor cores need 512.  In copies of
-// the kernel that leave out parts, under the same cap: 785 clocks where the sums are read but not added (887 us
-// at 1.42 GHz), 696 where finished buffers go straight back (832 us at 1.34 GHz).  So the summing warps are
-// a third of a block: their additions, of which half can stand among the reads because registers do not hold
-// a whole buffer beside the sums.  The 184 clocks that remain without them are not explained: products,
-// the 270 clocks until waiting warps see them done and the 370 until the leader sees the other CTA's
-// arrivals, over two buffers, make 576.  Ten warps are allocated as twelve, 168 registers each, and the
-// 256-column kernel spills inside of the loop (80 bytes of loads with bf16 results, 4 with fp32 ones).
+// What bounds it, on 4096 x 28672 x 8192 (25 rounds of 64 blocks on 74 pairs): 0.90 ms in a burst (2.1 PFLOP/s; 1.05 under the
+// power cap), 1.41 M clocks counted at 1.57 GHz, 884 a block, so either buffer is held for 1,768: for its
+// products (512, the full rate), 270 until the waiting warps see them done, 370 until the leader sees the other
+// CTA's arrivals, and some 610 for taking it into registers (half of the additions among the reads:
+// registers do not hold a whole buffer beside the sums).  Copies of the kernel that leave out parts agree: 684 a
+// block (0.75 ms) where the sums are read but not added, 617 (0.70 ms) where buffers go straight back, for
+// which products and hand-over predict 576.  Ten warps are allocated as twelve, 168 registers each, and
+// the 256-column kernel spills inside of the loop (80 bytes of loads with bf16 results, 4 with fp32 ones).
 // Tried and no faster: halves of 128 columns with their own buffers, 192 columns with all loads before the
 // additions, scales by another warp, results by TMA stores.
 #include <algorithm>
